@@ -456,6 +456,119 @@ NVFP4MOE_API int swiglu_backward(const float* gu, const float* dh, int64_t R_cap
 NVFP4MOE_API int bf16_transpose(const uint16_t* in, int64_t batches, int64_t rows, int64_t cols,
                                 uint16_t* out, void* stream);
 
+/*
+ * FP8 (E4M3fn) with one FP32 scale per 128 elements: a third precision beside
+ * NVFP4 and BF16 for the expert and dense products, forward or input gradient
+ * (the blog "miniTE NVFP4", section "Two complementary interventions": forward
+ * and backward precision are independent choices).
+ *   codes    uint8 [rows][K]             E4M3fn codes (largest value 448)
+ *   scales   float [ceil(K/128)][rows]   FP32 scale of each block of 128 elements
+ *                                        of a row (the last block of a row may be
+ *                                        shorter), block-major: the GEMM reads the
+ *                                        scales of consecutive rows as one run
+ *   weights: codes uint8 [E][N][K], scales float [E][ceil(N/128)][ceil(K/128)], one
+ *            per 128 x 128 block
+ *   value = e4m3(code) * scale
+ * Quantisation of a block: s = amax / 448 (FP32 division), code = E4M3(x / s)
+ * (FP32 quotient, nearest with ties to even, saturating at 448, sign kept; 0 if
+ * s == 0).  An all-zero block has s = 0.  amax ignores NaN; a NaN has a NaN code,
+ * and a block that holds an infinity has s = inf, NaN codes for its infinities
+ * and zero codes for its finite values, so either makes the products of its row NaN.
+ *
+ * fp8_quantize_rows - quantise `rows` rows of length K.
+ *   x        [rows][K] of x_dtype (NVFP4_IN_BF16 bits or NVFP4_IN_F32)
+ *   expert_offsets: if given, only rows [0, min(expert_offsets[E], rows)) are read
+ *            and written (E is unused otherwise)
+ *   codes    out [rows][K]; scales out [ceil(K/128)][rows]
+ * Requires K % 16 == 0, 16 <= K <= FP8_MAX_K, rows < 2^31.
+ *
+ * fp8_quantize_weights - quantise E matrices [N][K] by 128 x 128 blocks, in the
+ * stored order, transposed, or both in one pass over w:
+ *   codes    out [E][N][K], scales out [E][ceil(N/128)][ceil(K/128)] (both or neither)
+ *   codes_t  out [E][K][N], scales_t out [E][ceil(K/128)][ceil(N/128)] (both or neither):
+ *            the same codes and scales, transposed; the weight of the input-gradient
+ *            product dA = dC W, which contracts over N
+ * Requires K % 16 == 0, 16 <= K <= FP8_MAX_K, 1 <= N <= FP8_MAX_N, E <= 65535, at least
+ * one of codes and codes_t; with codes_t also N % 16 == 0, N <= FP8_MAX_K.
+ *
+ * fp8_swiglu_quantize - weighted SwiGLU of the gate_up output, quantised like
+ * fp8_quantize_rows (for the down product):
+ *   gu       [R_cap][2I] of gu_dtype (NVFP4_IN_BF16 or NVFP4_IN_F32): gate columns
+ *            [0, I), up columns [I, 2I)
+ *   topk_w, row_to_tk: as in swiglu_quantize (NULL topk_w: weight 1)
+ *   h = ((g / (1 + exp(-g))) * u) * w in FP32, each value within 2^-20 relative of
+ *       the exact one (plus 2^-149 |u w| where g sigmoid(g) is below the normal range)
+ *   codes [R_cap][I], scales [ceil(I/128)][R_cap]: FP8 of h
+ *   h_out    bf16 bits [R_cap][I], h rounded to nearest even (NULL: not written)
+ * Only rows below expert_offsets[E] are read and written.  Requires I % 16 == 0,
+ * 16 <= I <= FP8_MAX_K.
+ *
+ * fp8_grouped_gemm - grouped expert GEMM: for every expert e and row r in
+ * [offsets[e], offsets[e+1]):
+ *     c[r][n] = sum_j a_scales[j][r] * w_scales[e][n/128][j] * sum_{k in block j} a[r][k] w[e][n][k]
+ * E = 1 with expert_offsets = {0, M} is a dense product.  FP32 outputs: exact products
+ * of the codes and FP32 sums, within 2e-5 * sum_k |a_k w_k| per element.  BF16 outputs:
+ * the FP8 matrix instruction, which cuts the products of each 8 consecutive k off at
+ * 2^-13 of the largest of the 8 (some 1e-5 to 6e-5 of the result's 2-norm, at most
+ * 7 * 2^-13 * sum_k |a_k w_k| per element), then one rounding to bf16.  A row's bits do
+ * not depend on the other rows, on R_cap or on the routing.
+ *   a_codes [R_cap][K], a_scales [ceil(K/128)][R_cap]; w_codes [E][N][K], w_scales
+ *   [E][ceil(N/128)][ceil(K/128)]; c [R_cap][N] of c_dtype (NVFP4_OUT_F32, or
+ *   NVFP4_OUT_BF16: each FP32 result rounded to nearest even)
+ * Rows at or past expert_offsets[E] are neither read nor written.  Malformed offsets
+ * are clamped into [0, R_cap] (wrong rows, no access outside the buffers).
+ * Requires K % 16 == 0, 16 <= K <= FP8_MAX_K, 1 <= N <= FP8_MAX_N.
+ *
+ * fp8_grouped_gemm_gather - the same with the left operand gathered from token
+ * order: routed row r reads row row_to_tk[r] / k of a_codes [T][K] and a_scales
+ * [ceil(K/128)][T].  Requires T * K < 2^32, 1 <= k <= NVFP4MOE_MAX_TOPK; a map
+ * entry outside [0, T * k) reads a row clamped into [0, T).
+ */
+#define FP8_BLOCK 128
+#define FP8_MAX_K 65536
+#define FP8_MAX_N (1 << 20)
+NVFP4MOE_API int fp8_quantize_rows(const void* x, int32_t x_dtype, int64_t rows, int64_t K,
+                                   const int32_t* expert_offsets, int32_t E, uint8_t* codes,
+                                   float* scales, void* stream);
+NVFP4MOE_API int fp8_quantize_weights(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* codes,
+                                      float* scales, uint8_t* codes_t, float* scales_t, void* stream);
+NVFP4MOE_API int fp8_swiglu_quantize(const void* gu, int32_t gu_dtype, int64_t R_cap, int64_t I,
+                                     const int32_t* expert_offsets, int32_t E, const float* topk_w,
+                                     const int32_t* row_to_tk, uint8_t* codes, float* scales,
+                                     uint16_t* h_out, void* stream);
+NVFP4MOE_API int fp8_grouped_gemm(const uint8_t* a_codes, const float* a_scales,
+                                  const int32_t* expert_offsets, int32_t E, int64_t R_cap,
+                                  const uint8_t* w_codes, const float* w_scales, int64_t N, int64_t K,
+                                  void* c, int32_t c_dtype, void* stream);
+NVFP4MOE_API int fp8_grouped_gemm_gather(const uint8_t* a_codes, const float* a_scales, int64_t T,
+                                         const int32_t* row_to_tk, int32_t k,
+                                         const int32_t* expert_offsets, int32_t E, int64_t R_cap,
+                                         const uint8_t* w_codes, const float* w_scales, int64_t N,
+                                         int64_t K, void* c, int32_t c_dtype, void* stream);
+
+/*
+ * bf16_grouped_gemm_wgrad - the expert weight gradient in BF16 (the pair of the
+ * BF16 input gradient; nvfp4_grouped_gemm_wgrad is the NVFP4 one): for every
+ * expert e with rows [offsets[e], offsets[e+1]):
+ *     dW_e[m][n] = sum over its rows r of  g(r)[m] * x(r)[n]
+ * with FP32 sums; an expert without rows gets zeros.
+ *   g   bf16 bits [g_rows][M], the gradient of the expert GEMM's output; x bf16 bits
+ *       [x_rows][N], its input
+ *   g_k, x_k: 0 - the operand is in the expert-grouped order (g(r) is row r, at least
+ *       R_cap rows); k >= 1 - it is in token order and g(r) is row row_to_tk[r] / k
+ *       (a map entry outside the operand reads a row clamped into it)
+ *   row_to_tk int32 [R_cap]: needed if g_k or x_k
+ *   c   [E][M][N] of c_dtype: NVFP4_OUT_F32 (float) or NVFP4_OUT_BF16 (bf16 bits, each
+ *       FP32 result rounded to nearest even); every element is written
+ * Requires M % 8 == 0, N % 8 == 0, 8 <= M, N <= 2^20; an operand in token order under
+ * 4 GiB.
+ */
+NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int32_t g_k,
+                                         const uint16_t* x, int64_t x_rows, int32_t x_k,
+                                         const int32_t* row_to_tk, const int32_t* expert_offsets,
+                                         int32_t E, int64_t R_cap, int64_t M, int64_t N, void* c,
+                                         int32_t c_dtype, void* stream);
+
 /* Measurement aid (no part of the MoE computation): the device's practical
  * FP16 MFMA rate.  256 workgroups of 8 wavefronts (two per SIMD on a 256-CU
  * MI355X) each issue `iters` rounds of 8 independent v_mfma_f32_32x32x16_f16 on

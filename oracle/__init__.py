@@ -34,5 +34,6 @@ Modules:
   combine   - un-permutation with top-k combine, and the gather for dgrad
   layer     - the chained MoE layer forward and BF16 dgrad backward
   wgrad     - the expert weight gradient in NVFP4, quantised along tokens
+  fp8       - FP8 quantisation by blocks of 128, its grouped GEMM, the BF16 weight gradient
 """
-from . import formats, quantize, permute, gemm, swiglu, combine, layer, wgrad  # noqa: F401
+from . import formats, quantize, permute, gemm, swiglu, combine, layer, wgrad, fp8  # noqa: F401

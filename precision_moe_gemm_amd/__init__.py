@@ -9,7 +9,8 @@ stream only.  If the library has not been built, calls raise
 Tensor conventions: bf16 data may be passed as ``torch.bfloat16`` or as
 2-byte integer tensors holding the bits; NVFP4 codes and scales are
 ``torch.uint8``; row scales, GEMM outputs and router weights ``torch.float32``;
-routing ids, offsets and identity maps ``torch.int32``.
+routing ids, offsets and identity maps ``torch.int32``.  FP8 codes are ``torch.uint8`` or
+``torch.float8_e4m3fn``.
 """
 from __future__ import annotations
 
@@ -82,6 +83,14 @@ SIGNATURES = {
                                  _c.c_int),
     "swiglu_backward": ([_P, _P, _I64, _I64, _P, _I32, _P, _P, _P, _P], _c.c_int),
     "bf16_transpose": ([_P, _I64, _I64, _I64, _P, _P], _c.c_int),
+    "fp8_quantize_rows": ([_P, _I32, _I64, _I64, _P, _I32, _P, _P, _P], _c.c_int),
+    "fp8_quantize_weights": ([_P, _I64, _I64, _I64, _P, _P, _P, _P, _P], _c.c_int),
+    "fp8_swiglu_quantize": ([_P, _I32, _I64, _I64, _P, _I32, _P, _P, _P, _P, _P, _P], _c.c_int),
+    "fp8_grouped_gemm": ([_P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _I32, _P], _c.c_int),
+    "fp8_grouped_gemm_gather": ([_P, _P, _I64, _P, _I32, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _I32, _P],
+                                _c.c_int),
+    "bf16_grouped_gemm_wgrad": ([_P, _I64, _I32, _P, _I64, _I32, _P, _P, _I32, _I64, _I64, _I64, _P, _I32, _P],
+                                _c.c_int),
     "nvfp4moe_mfma_ceiling": ([_I64, _P, _P], _c.c_int),
 }
 
@@ -564,6 +573,186 @@ def swiglu_backward(gu, dh, expert_offsets, topk_w=None, row_to_tk=None, dgu=Non
         _ptr(gu), _ptr(dh), R_cap, I2 // 2, _ptr(expert_offsets), E, _ptr(topk_w),
         _ptr(row_to_tk), _ptr(dgu), _stream()))
     return dgu
+
+
+# ---------------------------------------------------------------------- FP8, 128 elements a scale
+FP8_BLOCK = 128
+_FP8 = (torch.uint8, torch.float8_e4m3fn)
+_OUT_DTYPES = {torch.float32: (OUT_F32, _F32), torch.bfloat16: (OUT_BF16, _BF16)}
+
+
+def _call(name, like, *args):
+    """The entry point on `like`'s device and that device's current stream."""
+    fn = getattr(load_library(), name)
+    if like.device.index == torch.cuda.current_device():
+        _check(name, fn(*args, _stream()))
+    else:
+        with torch.cuda.device(like.device):
+            _check(name, fn(*args, _stream()))
+
+
+def _same_device(like, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+
+
+def _in_dtype(t):
+    return 1 if t.dtype == torch.float32 else 0
+
+
+def _out(c, out_dtype, shape, like):
+    """The output tensor of an FP32 / BF16 product, and its dtype code."""
+    if out_dtype is None:
+        out_dtype = torch.float32 if c is None or c.dtype == torch.float32 else torch.bfloat16
+    if out_dtype not in _OUT_DTYPES:
+        raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
+    code, dtypes = _OUT_DTYPES[out_dtype]
+    c = _empty(shape, out_dtype, like) if c is None else c
+    _req(c, "c", dtypes, numel=math.prod(shape))
+    return c, code
+
+
+def _blocks(n):
+    return -(-n // FP8_BLOCK)
+
+
+def fp8_quantize_rows(x, expert_offsets=None, codes=None, scales=None):
+    """x bf16 or f32 [rows, K] -> (codes u8 [rows, K], scales f32 [ceil(K/128), rows]);
+    with expert_offsets only the routed rows [0, offsets[E]) are written."""
+    _req(x, "x", _BF16 + _F32, 2)
+    _req(expert_offsets, "expert_offsets", _I32T)
+    rows, K = x.shape
+    E = 0 if expert_offsets is None else expert_offsets.numel() - 1
+    codes = _empty((rows, K), torch.uint8, x) if codes is None else codes
+    scales = _empty((_blocks(K), rows), torch.float32, x) if scales is None else scales
+    _req(codes, "codes", _FP8, numel=rows * K)
+    _req(scales, "scales", _F32, numel=_blocks(K) * rows)
+    _same_device(x, expert_offsets=expert_offsets, codes=codes, scales=scales)
+    _call("fp8_quantize_rows", x, _ptr(x), _in_dtype(x), rows, K, _ptr(expert_offsets), E, _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def fp8_quantize_weights(w, transposed: bool = False, out=None):
+    """w bf16 [E, N, K] -> (codes u8 [E, N, K], scales f32 [E, ceil(N/128), ceil(K/128)]) by
+    128 x 128 blocks; with `transposed` also the same blocks of the transposed matrices,
+    (codes_t u8 [E, K, N], scales_t f32 [E, ceil(K/128), ceil(N/128)]), for the input gradient."""
+    _req(w, "w", _BF16, 3)
+    E, N, K = w.shape
+    o = out or {}
+    shapes = {"codes": (E, N, K), "scales": (E, _blocks(N), _blocks(K))}
+    if transposed:
+        shapes |= {"codes_t": (E, K, N), "scales_t": (E, _blocks(K), _blocks(N))}
+    res = []
+    for name, shp in shapes.items():
+        code = name.startswith("codes")
+        t = o[name] if name in o else _empty(shp, torch.uint8 if code else torch.float32, w)
+        _req(t, name, _FP8 if code else _F32, numel=math.prod(shp))
+        _same_device(w, **{name: t})
+        res.append(t)
+    _call("fp8_quantize_weights", w, _ptr(w), E, N, K, *[_ptr(t) for t in res], *[None] * (4 - len(res)))
+    return tuple(res)
+
+
+def fp8_swiglu_quantize(gu, expert_offsets, topk_w=None, row_to_tk=None, h_out=False, out=None):
+    """Weighted SwiGLU of gu bf16 or f32 [R_cap, 2I] + FP8 quantise of the routed rows.
+    Returns (codes u8 [R_cap, I], scales f32 [ceil(I/128), R_cap], h bf16 [R_cap, I] or None)."""
+    _req(gu, "gu", _BF16 + _F32, 2)
+    _req(expert_offsets, "expert_offsets", _I32T)
+    R_cap, I2 = gu.shape
+    if I2 % 2:
+        raise ValueError("gu must have 2 I columns")
+    I = I2 // 2
+    E = expert_offsets.numel() - 1
+    if topk_w is not None and row_to_tk is None:
+        raise ValueError("topk_w needs row_to_tk")
+    _req(topk_w, "topk_w", _F32, numel=R_cap)
+    _req(row_to_tk, "row_to_tk", _I32T, numel=R_cap)
+    o = out or {}
+    codes = o["codes"] if "codes" in o else _empty((R_cap, I), torch.uint8, gu)
+    scales = o["scales"] if "scales" in o else _empty((_blocks(I), R_cap), torch.float32, gu)
+    h = (o["h"] if "h" in o else _empty((R_cap, I), torch.bfloat16, gu)) if h_out else None
+    _req(codes, "codes", _FP8, numel=R_cap * I)
+    _req(scales, "scales", _F32, numel=_blocks(I) * R_cap)
+    _req(h, "h", _BF16, numel=R_cap * I)
+    _same_device(gu, expert_offsets=expert_offsets, topk_w=topk_w, row_to_tk=row_to_tk, codes=codes, scales=scales, h=h)
+    _call("fp8_swiglu_quantize", gu, _ptr(gu), _in_dtype(gu), R_cap, I, _ptr(expert_offsets), E, _ptr(topk_w),
+          _ptr(row_to_tk), _ptr(codes), _ptr(scales), _ptr(h))
+    return codes, scales, h
+
+
+def _fp8_operands(a_codes, a_scales, expert_offsets, w_codes, w_scales):
+    _req(a_codes, "a_codes", _FP8, 2)
+    _req(w_codes, "w_codes", _FP8, 3)
+    _req(expert_offsets, "expert_offsets", _I32T)
+    rows, K = a_codes.shape
+    E, N, kw = w_codes.shape
+    if kw != K or E != expert_offsets.numel() - 1:
+        raise ValueError("w_codes must be [E, N, K] for a_codes [rows, K] and expert_offsets [E + 1]")
+    _req(a_scales, "a_scales", _F32)
+    _req(w_scales, "w_scales", _F32)
+    if tuple(a_scales.shape) != (_blocks(K), rows):
+        raise ValueError(f"a_scales must be [ceil(K/128), rows] = {(_blocks(K), rows)}, got {tuple(a_scales.shape)}")
+    if tuple(w_scales.shape) != (E, _blocks(N), _blocks(K)):
+        raise ValueError(f"w_scales must be [E, ceil(N/128), ceil(K/128)] = {(E, _blocks(N), _blocks(K))}, "
+                         f"got {tuple(w_scales.shape)}")
+    return rows, K, E, N
+
+
+def fp8_grouped_gemm(a_codes, a_scales, expert_offsets, w_codes, w_scales, c=None, out_dtype=None):
+    """c[r] = dequant(A)[r] @ dequant(W_e).T over expert-grouped rows.  A: codes [R_cap, K], scales
+    [ceil(K/128), R_cap]; W: codes [E, N, K], scales [E, ceil(N/128), ceil(K/128)].
+    Returns [R_cap, N], float32 (default) or bfloat16 (out_dtype=torch.bfloat16, or a bf16 `c`)."""
+    rows, K, E, N = _fp8_operands(a_codes, a_scales, expert_offsets, w_codes, w_scales)
+    c, code = _out(c, out_dtype, (rows, N), a_codes)
+    _same_device(a_codes, a_scales=a_scales, expert_offsets=expert_offsets, w_codes=w_codes, w_scales=w_scales, c=c)
+    _call("fp8_grouped_gemm", a_codes, _ptr(a_codes), _ptr(a_scales), _ptr(expert_offsets), E, rows, _ptr(w_codes),
+          _ptr(w_scales), N, K, _ptr(c), code)
+    return c
+
+
+def fp8_grouped_gemm_gather(a_codes, a_scales, row_to_tk, k: int, expert_offsets, w_codes, w_scales, c=None,
+                            out_dtype=None):
+    """fp8_grouped_gemm whose left operand is in token order: routed row r reads row
+    row_to_tk[r] // k of A (codes [T, K], scales [ceil(K/128), T]).  Returns [R_cap, N]
+    for row_to_tk of R_cap entries."""
+    T, K, E, N = _fp8_operands(a_codes, a_scales, expert_offsets, w_codes, w_scales)
+    _req(row_to_tk, "row_to_tk", _I32T)
+    R_cap = row_to_tk.numel()
+    c, code = _out(c, out_dtype, (R_cap, N), a_codes)
+    _same_device(a_codes, a_scales=a_scales, row_to_tk=row_to_tk, expert_offsets=expert_offsets, w_codes=w_codes,
+                 w_scales=w_scales, c=c)
+    _call("fp8_grouped_gemm_gather", a_codes, _ptr(a_codes), _ptr(a_scales), T, _ptr(row_to_tk), k,
+          _ptr(expert_offsets), E, R_cap, _ptr(w_codes), _ptr(w_scales), N, K, _ptr(c), code)
+    return c
+
+
+def bf16_grouped_gemm_wgrad(g, x, expert_offsets, row_to_tk=None, k: int = 1, gather=None, c=None, out_dtype=None):
+    """dW [E, M, N] = per expert g_e.T @ x_e over its rows (zeros for an expert without rows),
+    float32 (default) or bfloat16.  g bf16 [rows, M], x bf16 [rows, N], in the expert-grouped
+    order, or with gather="g" / "x" / "both" in token order: routed row r is row
+    row_to_tk[r] // k of that operand."""
+    _req(g, "g", _BF16, 2)
+    _req(x, "x", _BF16, 2)
+    _req(expert_offsets, "expert_offsets", _I32T)
+    _req(row_to_tk, "row_to_tk", _I32T)
+    if gather not in (None, "g", "x", "both"):
+        raise ValueError('gather must be None, "g", "x" or "both"')
+    g_k, x_k = (k if gather in (name, "both") else 0 for name in ("g", "x"))
+    if gather is not None and (row_to_tk is None or k < 1):
+        raise ValueError("gather needs row_to_tk and k >= 1")
+    rows = [t.shape[0] for t, tk in ((g, g_k), (x, x_k)) if not tk]
+    if len(rows) == 2 and rows[0] != rows[1]:
+        raise ValueError("g and x must have the same rows")
+    R_cap = row_to_tk.numel() if gather is not None else rows[0]
+    if rows and rows[0] < R_cap:
+        raise ValueError(f"the expert-grouped operand has {rows[0]} rows, row_to_tk {R_cap} entries")
+    M, N, E = g.shape[1], x.shape[1], expert_offsets.numel() - 1
+    c, code = _out(c, out_dtype, (E, M, N), g)
+    _same_device(g, x=x, expert_offsets=expert_offsets, row_to_tk=row_to_tk, c=c)
+    _call("bf16_grouped_gemm_wgrad", g, _ptr(g), g.shape[0], g_k, _ptr(x), x.shape[0], x_k, _ptr(row_to_tk),
+          _ptr(expert_offsets), E, R_cap, M, N, _ptr(c), code)
+    return c
 
 
 def mfma_ceiling(iters: int, sink=None):
