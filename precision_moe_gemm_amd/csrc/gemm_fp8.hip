@@ -31,6 +31,8 @@ namespace g8 {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
@@ -84,33 +86,33 @@ __device__ __forceinline__ int off_at(const int32_t* __restrict__ offsets, int R
 
 // ------------------------------------------------------------------ many rows per expert
 // A workgroup of 8 wavefronts (2 x 4) computes up to BM x 256, a wavefront up to
-// 16 FM x 64 of it; the FP16 fragments of its 64 columns take 64 registers, so that
-// kernel's tiles are 192 rows high, the FP8 kernel's 256.
+// 16 FM x 64 of it.  BM is 256 for the FP8 kernel and 192 for the FP16 one, whose
+// fragments take twice the registers.
 constexpr int BN = 256, BK = kFp8Block;
-constexpr int kNumHeights = 4;
 constexpr int kTileCost = 96;                  // rows' worth of a tile's cost that does not scale with its rows
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int FN = 4, WN = 64;
 constexpr int kWI = BN / 8 / kWaves;           // weight load instructions per wavefront and K-step (8 rows each)
-constexpr int kStages = 2;
+constexpr int kWSlots = 2, kASlots = 2;        // K-steps in LDS
+constexpr uint32_t kOutOfRange = 0x80000000u;  // buffer offset that the range check drops
 
-template <bool F16>
-struct Shape {
-  static constexpr int FM = F16 ? 6 : 8, BM = 32 * FM;
-  static constexpr int kAI = BM / 8 / kWaves;             // activation load instructions per wavefront
-  static constexpr int kStageS = (BM + BN) * BK;          // scales follow the two operand tiles
-  static constexpr int kSaB = (BM * 4 + 255) & ~255;
-  static constexpr int kStageB = kStageS + kSaB + 256;
-  // tile heights to choose from, all multiples of 32
-  __host__ __device__ static constexpr int height(int i) { return i == 0 ? BM : i == 1 ? 3 * BM / 4 & ~31 : i == 2 ? 128 : 64; }
-};
+// Tile heights to choose from: BM and the smaller multiples of 64.
+constexpr int kNumHeights = 5;
+__host__ __device__ constexpr int height(int bm, int i) { return i == 0 ? bm : 64 * ((bm - 1) / 64 + 1 - i) > 64 ? 64 * ((bm - 1) / 64 + 1 - i) : 64; }
 
-template <bool F16>
+template <int FM>
 struct __align__(16) Smem {
-  uint8_t ring[kStages * Shape<F16>::kStageB];
-  int tile_start[NVFP4MOE_MAX_EXPERTS + 1];
+  static constexpr int BM = 32 * FM, kSaWaves = (BM + 63) / 64, kSa = 64 * kSaWaves;
+  uint8_t a[kASlots][BM * BK];
+  uint8_t w[kWSlots][BN * BK];
+  float sa[kASlots][kSa];
+  float sw[kASlots][64];      // two weight blocks' scales
+  int32_t map[2][kSa];        // gathered operand: the routing map of a tile's rows
+  int tile_start[NVFP4MOE_MAX_EXPERTS + 1];   // first m-tile of each expert
+  int off[NVFP4MOE_MAX_EXPERTS + 1];          // its first row
+  int64_t cost[kNumHeights];
 };
-static_assert(sizeof(Smem<false>) <= 160 * 1024 && sizeof(Smem<true>) <= 160 * 1024, "LDS");
+static_assert(sizeof(Smem<10>) <= 160 * 1024, "LDS");
 
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
@@ -125,44 +127,62 @@ __device__ __forceinline__ void lds_dma4(const void* base, uint32_t voff, uint32
 }
 #pragma clang diagnostic pop
 
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)p);
+}
+
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// fn(std::integral_constant<int, v>) for the v in Is... equal to n
-template <int... Is, typename Fn>
-__device__ __forceinline__ void dispatch_count(int n, std::integer_sequence<int, Is...>, Fn&& fn) {
-  (void)((n == Is ? (fn(std::integral_constant<int, Is>{}), true) : false) || ...);
+// Waits until at most n of this wavefront's loads and stores are outstanding (or
+// fewer: n is rounded down to one of the counts below).
+__device__ __forceinline__ void wait_vmcnt(int n) {
+#define G8_W(v) __builtin_amdgcn_s_waitcnt(0x0F70 | ((v) & 15) | ((v) >> 4 << 14))
+  if (n >= 16) G8_W(16);
+  else if (n >= 8) G8_W(8);
+  else if (n >= 4) G8_W(4);
+  else G8_W(0);
+#undef G8_W
 }
 
 struct Tile {
   int e, m0, rows, n0;
 };
 
-__device__ __forceinline__ Tile tile_at(int L, int n_tiles, const int* tile_start, int E,
-                                        const int32_t* __restrict__ offsets, int Rc) {
-  const int tm = L / n_tiles, tn = L - tm * n_tiles;
-  int lo = 0, hi = E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tile_start[mid] <= tm) lo = mid; else hi = mid;
-  }
+// Tile L; `from` is an expert at or before the tile's.  An expert's tiles run in
+// groups of kGroupM m-tiles, column by column: the 32 workgroups of an XCD, on
+// consecutive tiles, then share both operands' slabs in its L2.
+constexpr int kGroupM = 4;
+__device__ __forceinline__ Tile tile_at(int L, int from, int n_tiles, const int* tile_start, const int* offs, int E) {
+  const int tm = L / n_tiles, lane = lane_id();
+  // the last expert that starts at or before m-tile tm, 64 experts at a look
   Tile t;
-  t.e = __builtin_amdgcn_readfirstlane(lo);
+  t.e = from;
+  for (;;) {
+    const int x = t.e + 1 + lane;
+    const int n = __popcll(__ballot(x < E && tile_start[min(x, E)] <= tm));
+    t.e += n;
+    if (n < kWave) break;
+  }
+  const int o0 = __builtin_amdgcn_readfirstlane(offs[t.e]), o1 = __builtin_amdgcn_readfirstlane(offs[t.e + 1]);
+  const int s0 = __builtin_amdgcn_readfirstlane(tile_start[t.e]);
+  const int nt = __builtin_amdgcn_readfirstlane(tile_start[t.e + 1]) - s0;
+  const int idx = L - s0 * n_tiles, b = idx / (kGroupM * n_tiles), r = idx - b * kGroupM * n_tiles;
+  const int h = min(kGroupM, nt - b * kGroupM), tn = r / h;
   // the expert's rows split evenly over its m-tiles, in 16-row groups (no tile
   // is empty, none taller than the launch's height)
-  const int o0 = off_at(offsets, Rc, t.e), o1 = off_at(offsets, Rc, t.e + 1);
-  const int nt = tile_start[t.e + 1] - tile_start[t.e];
   const int per = ((o1 - o0 + nt - 1) / nt + 15) & ~15;
-  t.m0 = __builtin_amdgcn_readfirstlane(o0 + (tm - tile_start[t.e]) * per);
-  t.rows = __builtin_amdgcn_readfirstlane(max(0, min(per, o1 - t.m0)));
-  t.n0 = __builtin_amdgcn_readfirstlane(tn * BN);
+  t.m0 = o0 + (b * kGroupM + r - tn * h) * per;
+  t.rows = max(0, min(per, o1 - t.m0));
+  t.n0 = tn * BN;
   return t;
 }
 
-template <bool BF16OUT>
+// WHOLE: rows of c are whole 16-byte pieces
+template <bool BF16OUT, bool WHOLE, int FM>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, int a_rows,
                          const int32_t* __restrict__ a_map, int a_div,
@@ -170,44 +190,43 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
                          const uint8_t* __restrict__ w, const float* __restrict__ sw, int N, int K,
                          void* __restrict__ c) {
   constexpr bool F16 = !BF16OUT;
-  using S = Shape<F16>;
-  constexpr int FM = S::FM, BM = S::BM, kAI = S::kAI, kStageS = S::kStageS, kStageB = S::kStageB;
-  __shared__ Smem<F16> sm;
+  constexpr int BM = 32 * FM, kSaWaves = Smem<FM>::kSaWaves;
+  constexpr int kAI = (BM / 8 + kWaves - 1) / kWaves;   // activation load instructions per wavefront
+  __shared__ Smem<FM> sm;
   const int tid = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int l16 = lane & 15, g = lane >> 4;
   const int n_tiles = (N + BN - 1) / BN;
 
-  if (wave == 0) {
+  for (int e = tid; e <= E; e += kThreads) sm.off[e] = off_at(offsets, Rc, e);
+  __syncthreads();
+  if (wave < kNumHeights) {
     // Tile height: the candidate with the smallest estimated critical path,
-    // (tiles per workgroup) x (height + kTileCost).  Ties go to the taller.
+    // (tiles per workgroup) x (height + kTileCost); one wavefront each.
+    const int h = height(BM, wave);
+    int mt = 0;
+    for (int e = lane; e < E; e += kWave) mt += max(0, sm.off[e + 1] - sm.off[e] + h - 1) / h;
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) mt += __shfl_xor(mt, off, kWave);
     const int G = gridDim.x, xg = (G & 7) == 0 ? 8 : 1;
+    const int64_t per = ((int64_t)mt * n_tiles + xg - 1) / xg, wgs = G / xg;
+    if (lane == 0) sm.cost[wave] = (per + wgs - 1) / wgs * (h + kTileCost);
+  }
+  __syncthreads();
+  if (wave == 0) {
     int best = BM;
-    int64_t best_cost = INT64_MAX;
+    int64_t best_cost = sm.cost[0];
 #pragma unroll
-    for (int q = 0; q < kNumHeights; ++q) {
-      const int h = S::height(q);
-      int mt = 0;
-      for (int e0 = 0; e0 < E; e0 += kWave) {
-        const int e = e0 + lane;
-        int v = e < E ? max(0, off_at(offsets, Rc, e + 1) - off_at(offsets, Rc, e) + h - 1) / h : 0;
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
-        mt += v;
+    for (int q = 1; q < kNumHeights; ++q)   // ties go to the taller
+      if (sm.cost[q] < best_cost) {
+        best_cost = sm.cost[q];
+        best = height(BM, q);
       }
-      const int64_t total = (int64_t)mt * n_tiles;
-      const int64_t per = (total + xg - 1) / xg, wgs = G / xg;
-      const int64_t cost = (per + wgs - 1) / wgs * (h + kTileCost);
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = h;
-      }
-    }
     int carry = 0;
     for (int e0 = 0; e0 < E; e0 += kWave) {
       const int e = e0 + lane;
-      const int v = e < E ? max(0, off_at(offsets, Rc, e + 1) - off_at(offsets, Rc, e) + best - 1) / best : 0;
+      const int v = e < E ? max(0, sm.off[e + 1] - sm.off[e] + best - 1) / best : 0;
       int incl = v;
 #pragma unroll
       for (int off = 1; off < kWave; off <<= 1) {
@@ -237,69 +256,110 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
   if (begin >= end) return;
   const int nk = (K + BK - 1) / BK, tail = K & (BK - 1);
   const int nnb = (N + BK - 1) / BK;
+  auto find = [&](int L, int from) __attribute__((always_inline)) {
+    return tile_at(L, from, n_tiles, sm.tile_start, sm.off, E);
+  };
 
-  // ------------------------------------------------------------ load cursor
-  // (lL, lk): the next K-step to load.  A load instruction q of an operand fills
-  // 1 KiB, rows 8q .. 8q+7: lane i gives row 8q + i / 8, physical 16-byte chunk
-  // i % 8, which holds logical chunk (i % 8) ^ (row / 2 mod 8) (see mma_step).
-  // Wavefront v takes q = v, v + 8, ..; its lanes' logical chunk is the same in
-  // all of them.  The first kSaWaves wavefronts also load the scales of 64 rows
-  // each, the next one those of the tile's two weight column blocks.
-  constexpr int kSaWaves = S::kSaB / 256;
-  int lL = begin, lk = 0, l_rows = 0, l_cols = 0;
-  const uint8_t *pa = nullptr, *pw = nullptr;
-  const float* ps = nullptr;
-  uint32_t off_a[kAI], off_w[kWI], off_s = 0;
+  // ------------------------------------------------------------ loads
+  // A load instruction q of an operand fills 1 KiB, rows 8q .. 8q+7: lane i gives
+  // row 8q + i / 8, physical 16-byte chunk i % 8, which holds logical chunk
+  // (i % 8) ^ (row / 2 mod 8) (see mma_step).  Wavefront v takes q = v, v + 8, ..;
+  // its lanes' logical chunk is the same in all of them.
   const int chunk = 16 * ((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7));
   // the last K-step's chunks past K read the row's first chunk of that step
   // instead (in bounds); the compute side clears them
   const uint32_t back = tail && chunk >= tail ? chunk : 0;
-  auto set_load_tile = [&](int L) __attribute__((always_inline)) {
-    const Tile t = tile_at(L, n_tiles, sm.tile_start, E, offsets, Rc);
-    l_rows = t.rows;
-    l_cols = min(BN, N - t.n0);
-    // gathered operand: routed row m reads row a_map[m] / a_div of a, clamped
-    // into a (an invalid map entry reads a wrong row, never outside)
+  const int row8 = 8 * wave + (lane >> 3);
+
+  // Weights: the next K-step to load is step wk of tile wL, two steps ahead of
+  // the one being computed (w_cols = 0: no tile left).  The cursor moves to the
+  // next tile in next_w, outside the K-loop.
+  int wL = begin - step, wk = 0, w_e = 0, w_cols = 0;
+  const uint8_t* pw = w;
+  uint32_t off_w[kWI];
+  auto next_w = [&]() __attribute__((always_inline)) {
+    wL += step;
+    wk = 0;
+    w_cols = 0;
+    if (wL >= end) return;
+    const Tile t = find(wL, w_e);
+    w_e = t.e;
+    w_cols = min(BN, N - t.n0);
+#pragma unroll
+    for (int u = 0; u < kWI; ++u) off_w[u] = (uint32_t)min(row8 + 64 * u, w_cols - 1) * (uint32_t)K + chunk;
+    pw = w + ((int64_t)t.e * N + t.n0) * K;
+  };
+  auto issue_w = [&](int slot) __attribute__((always_inline)) -> int {   // returns the instructions issued
+    const uint32_t dst = lds_addr(sm.w[0]) + slot * (BN * BK) + wave * 1024;
+    const uint32_t bk = wk == nk - 1 ? back : 0;
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < kWI; ++u)
+      if (8 * wave + 64 * u < w_cols) {
+        lds_dma16(pw, off_w[u] - bk, dst + u * kWaves * 1024);
+        ++n;
+      }
+    pw += BK;
+    ++wk;
+    return n;
+  };
+
+  // Activations: step ak of tile at, one step ahead of the one being computed
+  // (at.rows = 0: no tile left).  The first kSaWaves wavefronts also load the
+  // scales of 64 rows each, the next one those of the tile's two weight column
+  // blocks.  A gathered operand's map entries for the tile after it are on their
+  // way into LDS meanwhile: row m of the tile reads row a_map[m] / a_div of a,
+  // clamped into a (an invalid entry reads a wrong row, never outside).
+  int aL = begin - step, ak = 0, abuf = 0;
+  Tile at{0, 0, 0, 0}, an = find(begin, 0);
+  const uint8_t* pa = a;
+  const float* ps = sa;
+  uint32_t off_a[kAI], off_s = 0;
+  auto issue_map = [&](const Tile& t, int buf) __attribute__((always_inline)) {
+    if (a_map && 64 * wave < t.rows)
+      lds_dma4(a_map + t.m0, 4 * min(64 * wave + lane, t.rows - 1), lds_addr(sm.map[0]) + (buf * Smem<FM>::kSa + 64 * wave) * 4);
+  };
+  auto next_a = [&]() __attribute__((always_inline)) {
+    aL += step;
+    ak = 0;
+    at.rows = 0;
+    if (aL >= end) return;
+    at = an;
     auto src = [&](int r) __attribute__((always_inline)) -> uint32_t {
-      const int m = min(r, t.rows - 1);
-      return a_map ? (uint32_t)min(max(a_map[t.m0 + m], 0) / a_div, a_rows - 1) : (uint32_t)m;
+      const int m = min(r, at.rows - 1);
+      return a_map ? (uint32_t)min(max(sm.map[abuf][m], 0) / a_div, a_rows - 1) : (uint32_t)m;
     };
 #pragma unroll
-    for (int u = 0; u < kAI; ++u) off_a[u] = src(8 * (wave + kWaves * u) + (lane >> 3)) * (uint32_t)K + chunk;
-#pragma unroll
-    for (int u = 0; u < kWI; ++u)
-      off_w[u] = (uint32_t)min(8 * (wave + kWaves * u) + (lane >> 3), l_cols - 1) * (uint32_t)K + chunk;
-    pa = a_map ? a : a + (int64_t)t.m0 * K;
-    pw = w + ((int64_t)t.e * N + t.n0) * K;
+    for (int u = 0; u < kAI; ++u) off_a[u] = src(row8 + 64 * u) * (uint32_t)K + chunk;
+    pa = a_map ? a : a + (int64_t)at.m0 * K;
     if (wave < kSaWaves) {
-      ps = a_map ? sa : sa + t.m0;
+      ps = a_map ? sa : sa + at.m0;
       off_s = 4 * src(64 * wave + lane);
     } else {
-      const int nb = t.n0 / BK;
-      ps = sw + ((int64_t)t.e * nnb + nb) * nk;
+      const int nb = at.n0 / BK;
+      ps = sw + ((int64_t)at.e * nnb + nb) * nk;
       off_s = 4 * nk * min(min(lane, 1), nnb - 1 - nb);
     }
+    abuf ^= 1;
+    if (aL + step < end) {
+      an = find(aL + step, at.e);
+      issue_map(an, abuf);
+    }
   };
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)sm.ring;
-  auto issue_loads = [&](int stage) __attribute__((always_inline)) {
-    if (lL >= end) return;
-    const uint32_t s0 = __builtin_amdgcn_readfirstlane(lds0 + stage * kStageB);
-    const uint32_t bk = lk == nk - 1 ? back : 0;
+  auto issue_a = [&](int slot) __attribute__((always_inline)) {
+    const uint32_t dst = lds_addr(sm.a[0]) + slot * (BM * BK) + wave * 1024;
+    const uint32_t bk = ak == nk - 1 ? back : 0;
 #pragma unroll
     for (int u = 0; u < kAI; ++u)
-      if (8 * (wave + kWaves * u) < l_rows) lds_dma16(pa, off_a[u] - bk, s0 + (wave + kWaves * u) * 1024);
-#pragma unroll
-    for (int u = 0; u < kWI; ++u)
-      if (8 * (wave + kWaves * u) < l_cols) lds_dma16(pw, off_w[u] - bk, s0 + BM * BK + (wave + kWaves * u) * 1024);
-    if (wave < kSaWaves ? 64 * wave < l_rows : wave == kSaWaves) lds_dma4(ps, off_s, s0 + kStageS + wave * 256);
-    pa += BK;
-    pw += BK;
-    ps += wave < kSaWaves ? a_rows : 1;
-    if (++lk == nk) {
-      lk = 0;
-      lL += step;
-      if (lL < end) set_load_tile(lL);
+      if (8 * wave + 64 * u < at.rows) lds_dma16(pa, off_a[u] - bk, dst + u * kWaves * 1024);
+    if (wave < kSaWaves) {
+      if (64 * wave < at.rows) lds_dma4(ps, off_s, lds_addr(sm.sa[0]) + (slot * Smem<FM>::kSa + 64 * wave) * 4);
+    } else if (wave == kSaWaves && at.rows > 0) {
+      lds_dma4(ps, off_s, lds_addr(sm.sw[0]) + slot * 256);
     }
+    pa += BK;
+    ps += wave < kSaWaves ? a_rows : 1;
+    ++ak;
   };
 
   floatx4 acc[FM][FN];
@@ -308,46 +368,92 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  // One K-step over the wavefront's first NF row fragments.  A fragment read
-  // gives lane (l16, g) the chunks g and g + 4 of row l16 of the fragment, each
-  // at its row's physical place, chunk ^ (row / 2 mod 8): a 16-byte LDS read is
-  // served 16 lanes at a time, here 16 rows with chunk g from one half and
-  // g ^ 1 from the other, and the XOR puts those on 16 different bank groups.
+  // Fragments.  A read gives lane (l16, g) the chunks g and g + 4 of row l16 of
+  // the fragment, each at its row's physical place, chunk ^ (row / 2 mod 8): a
+  // 16-byte LDS read is served 16 lanes at a time, here 16 rows with chunk g from
+  // one half and g ^ 1 from the other, and the XOR puts those on 16 different bank
+  // groups.  In a tile's last K-step the chunks past K are cleared in registers.
   const int pc0 = 16 * (g ^ (l16 >> 1)), pc1 = 16 * ((g + 4) ^ (l16 >> 1));
   auto frag = [&](const uint8_t* row) __attribute__((always_inline)) -> v8i {
     return join(*reinterpret_cast<const v4i*>(row + pc0), *reinterpret_cast<const v4i*>(row + pc1));
   };
-  auto mma_step = [&](auto nf_tag, int stage) __attribute__((always_inline)) {
-    constexpr int NF = decltype(nf_tag)::value;
-    if constexpr (NF > 0) {
-      const uint8_t* st = sm.ring + stage * kStageB;
-      const float* scales = reinterpret_cast<const float*>(st + kStageS);
-      const float swv = scales[S::kSaB / 4 + (wn >> 1)];
-      const uint8_t* wrow = st + (BM + WN * wn + l16) * BK;
-      const Frag<F16> wf[FN] = {Frag<F16>(frag(wrow)), Frag<F16>(frag(wrow + 16 * BK)), Frag<F16>(frag(wrow + 32 * BK)),
-                                Frag<F16>(frag(wrow + 48 * BK))};
-      floatx4 p[FN];
-      float s = 0.0f;
+  auto clear_tail = [&](v8i& f) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i <= NF; ++i) {
-        floatx4 q[FN];
-        float sn = 0.0f;
-        if (i < NF) {
-          const int r = 32 * i + 16 * wm + l16;
-          const Frag<F16> av(frag(st + r * BK));
-          sn = scales[r] * swv;
+    for (int x = 0; x < 8; ++x) f[x] = 16 * (g + (x & 4)) < tail ? f[x] : 0;
+  };
+  // One K-step.  Row fragments go FB at a time: a group past the wavefront's rows
+  // is skipped, a partial one computed whole (the stage's other rows are whatever
+  // it held, their results are never stored); the next group's reads are issued
+  // before this one's matrix instructions.
+  constexpr int FB = F16 || FM > 8 ? 1 : 2;
+  auto mma_step = [&](int slot, int nf, bool clear) __attribute__((always_inline)) {
+    const uint8_t* wrow = sm.w[0] + slot * (BN * BK) + (WN * wn + l16) * BK;
+    const uint8_t* arow = sm.a[0] + slot * (BM * BK) + (16 * wm + l16) * BK;
+    const float* sav = sm.sa[0] + slot * Smem<FM>::kSa + 16 * wm + l16;
+    v8i wr[FN], ar[FB];
+    float sr[FB];
+    wr[0] = frag(wrow);
 #pragma unroll
-          for (int j = 0; j < FN; ++j) q[j] = block_sum(wf[j], av);
+    for (int f = 0; f < FB; ++f) {
+      ar[f] = frag(arow + 32 * f * BK);
+      sr[f] = sav[32 * f];
+    }
+#pragma unroll
+    for (int j = 1; j < FN; ++j) wr[j] = frag(wrow + 16 * j * BK);
+    const float swv = sm.sw[slot][wn >> 1];
+    if (clear) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) clear_tail(wr[j]);
+    }
+    const Frag<F16> wf[FN] = {Frag<F16>(wr[0]), Frag<F16>(wr[1]), Frag<F16>(wr[2]), Frag<F16>(wr[3])};
+#pragma unroll
+    for (int b = 0; b < FM; b += FB) {
+      if (b < nf) {
+        v8i an_[FB];
+        float sn[FB];
+        if (b + FB < FM) {
+#pragma unroll
+          for (int f = 0; f < FB; ++f) {
+            an_[f] = frag(arow + 32 * (b + FB + f) * BK);
+            sn[f] = sav[32 * (b + FB + f)];
+          }
         }
-        if (i > 0) {
+        floatx4 p[FB][FN];
+#pragma unroll
+        for (int f = 0; f < FB; ++f) {
+          const Frag<F16> av(ar[f]);
+#pragma unroll
+          for (int j = 0; j < FN; ++j) p[f][j] = block_sum(wf[j], av);
+        }
+#pragma unroll
+        for (int f = 0; f < FB; ++f) {
+          const float s = sr[f] * swv;
 #pragma unroll
           for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) acc[i - 1][j][v] = __builtin_fmaf(p[j][v], s, acc[i - 1][j][v]);
+            for (int v = 0; v < 4; ++v) acc[b + f][j][v] = __builtin_fmaf(p[f][j][v], s, acc[b + f][j][v]);
         }
+        if constexpr (!F16) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 6 * FB, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) p[j] = q[j];
-        s = sn;
+          for (int t = 2; t < FB * FN; ++t) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // the FMAs of an earlier one
+          }
+          __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+        }
+        // the sums are complete here (otherwise the compiler sinks the FMAs into
+        // the next step, holding the products' registers until then)
+#pragma unroll
+        for (int f = 0; f < FB; ++f)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[b + f][j]));
+#pragma unroll
+        for (int f = 0; f < FB; ++f) {
+          ar[f] = an_[f];
+          sr[f] = sn[f];
+        }
       }
     }
   };
@@ -355,87 +461,106 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
   // Lane (l16, g) of tile (i, j) holds tile row 32i + 16wm + l16 (the two
   // wavefront rows take alternate 16-row groups, so a partial tile splits
   // evenly), columns 16j + 4g .. +3 of the wavefront's 64.  Rows past the tile's
-  // and columns past N are not written.  The accumulators are cleared.
-  const bool whole4 = (N & 3) == 0;
-  auto epilogue = [&](const Tile& t) __attribute__((always_inline)) {
+  // and columns past N go to buffer offsets that the range check drops, so the
+  // number of store instructions is known and the next wait can leave them in
+  // flight.  BF16: a lane pair's halves of two fragments' 8-column pieces are
+  // exchanged first, so that a lane stores 16 bytes.  Returns the stores (0: not
+  // known, the scalar path).  The accumulators are cleared.
+  constexpr int kOutB = BF16OUT ? 2 : 4;
+  auto epilogue = [&](const Tile& t) __attribute__((always_inline)) -> int {
+    const int nf = (t.rows + 31) >> 5;   // row fragments that hold rows, for either wavefront row
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        static_cast<uint8_t*>(c) + (int64_t)t.m0 * N * kOutB, (short)0, t.rows * N * kOutB, 0x00020000);
+    uint32_t row_off = (uint32_t)((16 * wm + l16) * N);   // opaque: not hoisted out of the tile loop
+    asm volatile("" : "+v"(row_off));
+    const int n0 = t.n0 + WN * wn;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int r = 32 * i + 16 * wm + l16;
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int n = t.n0 + WN * wn + 16 * j + 4 * g;
-        const int64_t at = (int64_t)(t.m0 + r) * N + n;
-        if (r < t.rows && n < N) {
-          const floatx4 v = acc[i][j];
+      if (i < nf) {
+        const uint32_t ro = row_off + (uint32_t)(32 * i * N);
+        if constexpr (WHOLE) {
           if constexpr (BF16OUT) {
-            uint16_t* p = static_cast<uint16_t*>(c) + at;
-            const uint32_t lo = bf16x2_rne(v[0], v[1]), hi = bf16x2_rne(v[2], v[3]);
-            if (whole4) {
-              *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
-            } else {
-              p[0] = (uint16_t)lo;
-              if (n + 1 < N) p[1] = (uint16_t)(lo >> 16);
-              if (n + 2 < N) p[2] = (uint16_t)hi;
-              if (n + 3 < N) p[3] = (uint16_t)(hi >> 16);
+#pragma unroll
+            for (int j = 0; j < FN; j += 2) {
+              const floatx4 x = acc[i][j], y = acc[i][j + 1];
+              const v2u lo = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane16_swap(bf16x2_rne(x[0], x[1]), bf16x2_rne(y[0], y[1]), false, false));
+              const v2u hi = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane16_swap(bf16x2_rne(x[2], x[3]), bf16x2_rne(y[2], y[3]), false, false));
+              const int n = n0 + 16 * (j + (g & 1)) + 8 * (g >> 1);
+              __builtin_amdgcn_raw_buffer_store_b128((v4u){lo[0], hi[0], lo[1], hi[1]}, rsrc,
+                                                     n < N ? (ro + (uint32_t)n) * 2u : kOutOfRange, 0, 0);
             }
           } else {
-            float* p = static_cast<float*>(c) + at;
-            if (whole4) {
-              *reinterpret_cast<floatx4*>(p) = v;
-            } else {
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (n + x < N) p[x] = v[x];
+            for (int j = 0; j < FN; ++j) {
+              const int n = n0 + 16 * j + 4 * g;
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[i][j]), rsrc,
+                                                     n < N ? (ro + (uint32_t)n) * 4u : kOutOfRange, 0, 0);
             }
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int n = n0 + 16 * j + 4 * g + v;
+              const uint32_t o = n < N ? (ro + (uint32_t)n) * kOutB : kOutOfRange;
+              if constexpr (BF16OUT)
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bf16x2_rne(acc[i][j][v], 0.0f), rsrc, o, 0, 0);
+              else
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][v]), rsrc, o, 0, 0);
+            }
         }
-        acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
       }
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
+    return WHOLE ? nf * (BF16OUT ? FN / 2 : FN) : 0;
   };
 
   // ------------------------------------------------------------ pipeline
-  // At the top of a K-step its loads have landed (this wavefront's by the wait,
-  // everyone's by the barrier); the other stage, read in the step before, takes
-  // the next step's loads, which fly while this step computes.
-  set_load_tile(begin);
-  issue_loads(0);
-  int sc = 0;
-  auto top = [&](int kt) __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+  // Top of K-step s: its loads have landed (this wavefront's by the wait, everyone's
+  // by the barrier; only stores may be in flight); the other slots, read in the step
+  // before, take the loads of s + 1, which fly while this step computes.  A tile's
+  // stores follow those loads in the first step of the next tile.
+  int slot = 0, st = 0;
+  auto begin_loads = [&](int to) __attribute__((always_inline)) {
+    if (wk == nk) next_w();
+    if (ak == nk) next_a();   // its map entries were loaded at least a step ago
+    (void)issue_w(to);
+    issue_a(to);
+  };
+  issue_map(an, 0);
+  if (a_map) {
+    wait_vmcnt(0);
     lds_barrier();
-    issue_loads(sc ^ 1);
-    if (tail && kt == nk - 1) {
-      // clear the chunks past K of both operands (the other stage is untouched)
-      const int first = tail / 16;
-      for (int i = tid; i < (BM + BN) * 8; i += kThreads) {
-        const int r = i >> 3, pc = i & 7;
-        if ((pc ^ ((r >> 1) & 7)) >= first)
-          *reinterpret_cast<uint4*>(sm.ring + sc * kStageB + r * BK + pc * 16) = make_uint4(0, 0, 0, 0);
-      }
-      lds_barrier();
-    }
-  };
-  auto run_tile = [&](auto nf_tag) __attribute__((always_inline)) {
-    mma_step(nf_tag, sc);   // K-step 0: its top is done by the caller
-    sc ^= 1;
-    for (int kt = 1; kt < nk; ++kt) {
-      top(kt);
-      mma_step(nf_tag, sc);
-      sc ^= 1;
-    }
-  };
+  }
+  wk = ak = nk;
+  begin_loads(0);
   Tile prev{0, 0, 0, 0};
   for (int L = begin; L < end; L += step) {
-    const Tile t = tile_at(L, n_tiles, sm.tile_start, E, offsets, Rc);
-    top(0);
-    epilogue(prev);   // before the first tile: no rows, nothing is written
+    const Tile t = find(L, prev.e);
     const int nf = min(FM, (((t.rows + 15) >> 4) - wm + 1) >> 1);
-    dispatch_count(nf, std::make_integer_sequence<int, FM + 1>{},
-                   [&](auto nf_tag) __attribute__((always_inline)) { run_tile(nf_tag); });
+    for (int kt = 0; kt < nk; ++kt) {
+      wait_vmcnt(st);
+      st = 0;
+      lds_barrier();
+      begin_loads(slot ^ 1);
+      const bool clear = tail && kt == nk - 1;
+      if (clear) {   // the activations' chunks past K (the weights' are cleared in registers)
+        const int first = tail / 16;
+        for (int i = tid; i < BM * 8; i += kThreads) {
+          const int r = i >> 3, pc = i & 7;
+          if ((pc ^ ((r >> 1) & 7)) >= first) *reinterpret_cast<uint4*>(sm.a[slot] + r * BK + pc * 16) = make_uint4(0, 0, 0, 0);
+        }
+        lds_barrier();
+      }
+      if (kt == 0) st = epilogue(prev);   // before the first tile: no rows, nothing is written
+      mma_step(slot, nf, clear);
+      slot ^= 1;
+    }
     prev = t;
   }
-  epilogue(prev);
+  (void)epilogue(prev);
 }
 
 // ------------------------------------------------------------------ few rows per expert
@@ -559,25 +684,26 @@ int launch(const uint8_t* a, const float* sa, int64_t a_rows, const int32_t* a_m
   if (!aligned16(a) || !aligned16(sa) || !aligned16(w) || !aligned16(sw) || !aligned16(c)) return NVFP4_ERR_ALIGN;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool bf = c_dtype == NVFP4_OUT_BF16;
-#define FP8_GEMM(KERNEL, GRID, THREADS)                                                                       \
-  (bf ? KERNEL<true><<<GRID, THREADS, 0, s>>>(a, sa, (int)a_rows, a_map, a_div, offsets, E, (int)R_cap, w, sw, \
-                                              (int)N, (int)K, c)                                              \
-      : KERNEL<false><<<GRID, THREADS, 0, s>>>(a, sa, (int)a_rows, a_map, a_div, offsets, E, (int)R_cap, w, sw, \
-                                               (int)N, (int)K, c))
+#define FP8_GEMM(KERNEL, GRID, THREADS) \
+  KERNEL<<<GRID, THREADS, 0, s>>>(a, sa, (int)a_rows, a_map, a_div, offsets, E, (int)R_cap, w, sw, (int)N, (int)K, c)
   if (R_cap <= 16 * (int64_t)E || R_cap <= 64) {
     // sum of ceil(rows / 16) over the experts is at most this
     const int64_t mt = std::min(R_cap, R_cap / g8::kRowsH + E);
     const dim3 grid((unsigned)((N + g8::kRowsN - 1) / g8::kRowsN), (unsigned)mt);
-    FP8_GEMM(g8::rows_kernel, grid, g8::kRowsWaves * 64);
+    if (bf) FP8_GEMM(g8::rows_kernel<true>, grid, g8::kRowsWaves * 64);
+    else FP8_GEMM(g8::rows_kernel<false>, grid, g8::kRowsWaves * 64);
     return launch_status();
   }
   const int64_t n_tiles = (N + g8::BN - 1) / g8::BN;
-  const int64_t min_h = g8::Shape<false>::height(g8::kNumHeights - 1);
-  const int64_t max_tiles = ((R_cap + min_h - 1) / min_h + E) * n_tiles;
+  constexpr int kFM8 = 8, kFM16 = 6;
+  const int64_t max_tiles = ((R_cap + 63) / 64 + E) * n_tiles;
   if (max_tiles > INT32_MAX) return NVFP4_ERR_SHAPE;
   int64_t grid = max_tiles < 256 ? max_tiles : 256;   // one workgroup per CU, a multiple of 8
   if (grid >= 8) grid &= ~7ll;
-  FP8_GEMM(g8::grouped_gemm_kernel, (unsigned)grid, g8::kThreads);
+  if (bf && N % 8 == 0) FP8_GEMM((g8::grouped_gemm_kernel<true, true, kFM8>), (unsigned)grid, g8::kThreads);
+  else if (bf) FP8_GEMM((g8::grouped_gemm_kernel<true, false, kFM8>), (unsigned)grid, g8::kThreads);
+  else if (N % 4 == 0) FP8_GEMM((g8::grouped_gemm_kernel<false, true, kFM16>), (unsigned)grid, g8::kThreads);
+  else FP8_GEMM((g8::grouped_gemm_kernel<false, false, kFM16>), (unsigned)grid, g8::kThreads);
 #undef FP8_GEMM
   return launch_status();
 }
