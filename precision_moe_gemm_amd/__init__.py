@@ -578,39 +578,58 @@ def swiglu_backward(gu, dh, expert_offsets, topk_w=None, row_to_tk=None, dgu=Non
 # ---------------------------------------------------------------------- FP8, 128 elements a scale
 FP8_BLOCK = 128
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
+_BF16_F32 = _BF16 + _F32
 _OUT_DTYPES = {torch.float32: (OUT_F32, _F32), torch.bfloat16: (OUT_BF16, _BF16)}
 
 
-def _call(name, like, *args):
-    """The entry point on `like`'s device and that device's current stream."""
-    fn = getattr(load_library(), name)
-    if like.device.index == torch.cuda.current_device():
-        _check(name, fn(*args, _stream()))
+def _call(name, dev, *args):
+    """The entry point on device `dev` (an index) and that device's current stream.
+
+    Small calls are bound by the host, so this asks torch for the raw stream
+    (torch.cuda.current_stream builds an object around it first)."""
+    fn = getattr(_LIB or load_library(), name)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(like.device):
-            _check(name, fn(*args, _stream()))
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(name, status)
 
 
-def _same_device(like, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+def _arg(t, name, dtypes, dev, ndim=None, numel=None):
+    """_req of a tensor that must be there, and that it lies on device `dev`."""
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    _req(t, name, dtypes, ndim, numel)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
-def _in_dtype(t):
-    return 1 if t.dtype == torch.float32 else 0
+def _head(t, name, dtypes, ndim):
+    """_req of the argument whose device the call runs on; returns that device's index."""
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    _req(t, name, dtypes, ndim)
+    return t.get_device()
 
 
-def _out(c, out_dtype, shape, like):
-    """The output tensor of an FP32 / BF16 product, and its dtype code."""
+def _give(t, name, shape, dtype, dtypes, like, dev):
+    """An output: the caller's tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _arg(t, name, dtypes, dev, numel=math.prod(shape))
+    return t
+
+
+def _out_dtype(c, out_dtype):
+    """(torch dtype, accepted dtypes, dtype code) of an FP32 / BF16 product's output."""
     if out_dtype is None:
         out_dtype = torch.float32 if c is None or c.dtype == torch.float32 else torch.bfloat16
     if out_dtype not in _OUT_DTYPES:
         raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
     code, dtypes = _OUT_DTYPES[out_dtype]
-    c = _empty(shape, out_dtype, like) if c is None else c
-    _req(c, "c", dtypes, numel=math.prod(shape))
-    return c, code
+    return out_dtype, dtypes, code
 
 
 def _blocks(n):
@@ -620,16 +639,16 @@ def _blocks(n):
 def fp8_quantize_rows(x, expert_offsets=None, codes=None, scales=None):
     """x bf16 or f32 [rows, K] -> (codes u8 [rows, K], scales f32 [ceil(K/128), rows]);
     with expert_offsets only the routed rows [0, offsets[E]) are written."""
-    _req(x, "x", _BF16 + _F32, 2)
-    _req(expert_offsets, "expert_offsets", _I32T)
+    dev = _head(x, "x", _BF16_F32, 2)
     rows, K = x.shape
-    E = 0 if expert_offsets is None else expert_offsets.numel() - 1
-    codes = _empty((rows, K), torch.uint8, x) if codes is None else codes
-    scales = _empty((_blocks(K), rows), torch.float32, x) if scales is None else scales
-    _req(codes, "codes", _FP8, numel=rows * K)
-    _req(scales, "scales", _F32, numel=_blocks(K) * rows)
-    _same_device(x, expert_offsets=expert_offsets, codes=codes, scales=scales)
-    _call("fp8_quantize_rows", x, _ptr(x), _in_dtype(x), rows, K, _ptr(expert_offsets), E, _ptr(codes), _ptr(scales))
+    E = 0
+    if expert_offsets is not None:
+        _arg(expert_offsets, "expert_offsets", _I32T, dev)
+        E = expert_offsets.numel() - 1
+    codes = _give(codes, "codes", (rows, K), torch.uint8, _FP8, x, dev)
+    scales = _give(scales, "scales", (_blocks(K), rows), torch.float32, _F32, x, dev)
+    _call("fp8_quantize_rows", dev, x.data_ptr(), x.dtype == torch.float32, rows, K, _ptr(expert_offsets), E,
+          codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -637,77 +656,70 @@ def fp8_quantize_weights(w, transposed: bool = False, out=None):
     """w bf16 [E, N, K] -> (codes u8 [E, N, K], scales f32 [E, ceil(N/128), ceil(K/128)]) by
     128 x 128 blocks; with `transposed` also the same blocks of the transposed matrices,
     (codes_t u8 [E, K, N], scales_t f32 [E, ceil(K/128), ceil(N/128)]), for the input gradient."""
-    _req(w, "w", _BF16, 3)
+    dev = _head(w, "w", _BF16, 3)
     E, N, K = w.shape
+    nb, kb = _blocks(N), _blocks(K)
     o = out or {}
-    shapes = {"codes": (E, N, K), "scales": (E, _blocks(N), _blocks(K))}
+    res = (_give(o.get("codes"), "codes", (E, N, K), torch.uint8, _FP8, w, dev),
+           _give(o.get("scales"), "scales", (E, nb, kb), torch.float32, _F32, w, dev))
     if transposed:
-        shapes |= {"codes_t": (E, K, N), "scales_t": (E, _blocks(K), _blocks(N))}
-    res = []
-    for name, shp in shapes.items():
-        code = name.startswith("codes")
-        t = o[name] if name in o else _empty(shp, torch.uint8 if code else torch.float32, w)
-        _req(t, name, _FP8 if code else _F32, numel=math.prod(shp))
-        _same_device(w, **{name: t})
-        res.append(t)
-    _call("fp8_quantize_weights", w, _ptr(w), E, N, K, *[_ptr(t) for t in res], *[None] * (4 - len(res)))
-    return tuple(res)
+        res += (_give(o.get("codes_t"), "codes_t", (E, K, N), torch.uint8, _FP8, w, dev),
+                _give(o.get("scales_t"), "scales_t", (E, kb, nb), torch.float32, _F32, w, dev))
+    _call("fp8_quantize_weights", dev, w.data_ptr(), E, N, K, *[t.data_ptr() for t in res], *[None] * (4 - len(res)))
+    return res
 
 
 def fp8_swiglu_quantize(gu, expert_offsets, topk_w=None, row_to_tk=None, h_out=False, out=None):
     """Weighted SwiGLU of gu bf16 or f32 [R_cap, 2I] + FP8 quantise of the routed rows.
     Returns (codes u8 [R_cap, I], scales f32 [ceil(I/128), R_cap], h bf16 [R_cap, I] or None)."""
-    _req(gu, "gu", _BF16 + _F32, 2)
-    _req(expert_offsets, "expert_offsets", _I32T)
+    dev = _head(gu, "gu", _BF16_F32, 2)
+    _arg(expert_offsets, "expert_offsets", _I32T, dev)
     R_cap, I2 = gu.shape
     if I2 % 2:
         raise ValueError("gu must have 2 I columns")
     I = I2 // 2
-    E = expert_offsets.numel() - 1
-    if topk_w is not None and row_to_tk is None:
-        raise ValueError("topk_w needs row_to_tk")
-    _req(topk_w, "topk_w", _F32, numel=R_cap)
-    _req(row_to_tk, "row_to_tk", _I32T, numel=R_cap)
+    if topk_w is not None:
+        if row_to_tk is None:
+            raise ValueError("topk_w needs row_to_tk")
+        _arg(topk_w, "topk_w", _F32, dev, numel=R_cap)
+        _arg(row_to_tk, "row_to_tk", _I32T, dev, numel=R_cap)
     o = out or {}
-    codes = o["codes"] if "codes" in o else _empty((R_cap, I), torch.uint8, gu)
-    scales = o["scales"] if "scales" in o else _empty((_blocks(I), R_cap), torch.float32, gu)
-    h = (o["h"] if "h" in o else _empty((R_cap, I), torch.bfloat16, gu)) if h_out else None
-    _req(codes, "codes", _FP8, numel=R_cap * I)
-    _req(scales, "scales", _F32, numel=_blocks(I) * R_cap)
-    _req(h, "h", _BF16, numel=R_cap * I)
-    _same_device(gu, expert_offsets=expert_offsets, topk_w=topk_w, row_to_tk=row_to_tk, codes=codes, scales=scales, h=h)
-    _call("fp8_swiglu_quantize", gu, _ptr(gu), _in_dtype(gu), R_cap, I, _ptr(expert_offsets), E, _ptr(topk_w),
-          _ptr(row_to_tk), _ptr(codes), _ptr(scales), _ptr(h))
+    codes = _give(o.get("codes"), "codes", (R_cap, I), torch.uint8, _FP8, gu, dev)
+    scales = _give(o.get("scales"), "scales", (_blocks(I), R_cap), torch.float32, _F32, gu, dev)
+    h = _give(o.get("h"), "h", (R_cap, I), torch.bfloat16, _BF16, gu, dev) if h_out else None
+    _call("fp8_swiglu_quantize", dev, gu.data_ptr(), gu.dtype == torch.float32, R_cap, I, _ptr(expert_offsets),
+          expert_offsets.numel() - 1, _ptr(topk_w), _ptr(row_to_tk), codes.data_ptr(), scales.data_ptr(), _ptr(h))
     return codes, scales, h
 
 
 def _fp8_operands(a_codes, a_scales, expert_offsets, w_codes, w_scales):
-    _req(a_codes, "a_codes", _FP8, 2)
-    _req(w_codes, "w_codes", _FP8, 3)
-    _req(expert_offsets, "expert_offsets", _I32T)
+    dev = _head(a_codes, "a_codes", _FP8, 2)
+    _arg(w_codes, "w_codes", _FP8, dev, 3)
+    _arg(expert_offsets, "expert_offsets", _I32T, dev)
     rows, K = a_codes.shape
     E, N, kw = w_codes.shape
     if kw != K or E != expert_offsets.numel() - 1:
         raise ValueError("w_codes must be [E, N, K] for a_codes [rows, K] and expert_offsets [E + 1]")
-    _req(a_scales, "a_scales", _F32)
-    _req(w_scales, "w_scales", _F32)
-    if tuple(a_scales.shape) != (_blocks(K), rows):
-        raise ValueError(f"a_scales must be [ceil(K/128), rows] = {(_blocks(K), rows)}, got {tuple(a_scales.shape)}")
-    if tuple(w_scales.shape) != (E, _blocks(N), _blocks(K)):
-        raise ValueError(f"w_scales must be [E, ceil(N/128), ceil(K/128)] = {(E, _blocks(N), _blocks(K))}, "
+    _arg(a_scales, "a_scales", _F32, dev)
+    _arg(w_scales, "w_scales", _F32, dev)
+    kb = _blocks(K)
+    if tuple(a_scales.shape) != (kb, rows):
+        raise ValueError(f"a_scales must be [ceil(K/128), rows] = {(kb, rows)}, got {tuple(a_scales.shape)}")
+    if tuple(w_scales.shape) != (E, _blocks(N), kb):
+        raise ValueError(f"w_scales must be [E, ceil(N/128), ceil(K/128)] = {(E, _blocks(N), kb)}, "
                          f"got {tuple(w_scales.shape)}")
-    return rows, K, E, N
+    return dev, rows, K, E, N
 
 
 def fp8_grouped_gemm(a_codes, a_scales, expert_offsets, w_codes, w_scales, c=None, out_dtype=None):
     """c[r] = dequant(A)[r] @ dequant(W_e).T over expert-grouped rows.  A: codes [R_cap, K], scales
     [ceil(K/128), R_cap]; W: codes [E, N, K], scales [E, ceil(N/128), ceil(K/128)].
     Returns [R_cap, N], float32 (default) or bfloat16 (out_dtype=torch.bfloat16, or a bf16 `c`)."""
-    rows, K, E, N = _fp8_operands(a_codes, a_scales, expert_offsets, w_codes, w_scales)
-    c, code = _out(c, out_dtype, (rows, N), a_codes)
-    _same_device(a_codes, a_scales=a_scales, expert_offsets=expert_offsets, w_codes=w_codes, w_scales=w_scales, c=c)
-    _call("fp8_grouped_gemm", a_codes, _ptr(a_codes), _ptr(a_scales), _ptr(expert_offsets), E, rows, _ptr(w_codes),
-          _ptr(w_scales), N, K, _ptr(c), code)
+    dev, rows, K, E, N = _fp8_operands(a_codes, a_scales, expert_offsets, w_codes, w_scales)
+    dt, dtypes, code = _out_dtype(c, out_dtype)
+    c = _give(c, "c", (rows, N), dt, dtypes, a_codes, dev)
+    _call("fp8_grouped_gemm", dev, a_codes.data_ptr(), a_scales.data_ptr(), expert_offsets.data_ptr(), E, rows,
+          w_codes.data_ptr(), w_scales.data_ptr(), N, K, c.data_ptr(), code)
     return c
 
 
@@ -716,14 +728,13 @@ def fp8_grouped_gemm_gather(a_codes, a_scales, row_to_tk, k: int, expert_offsets
     """fp8_grouped_gemm whose left operand is in token order: routed row r reads row
     row_to_tk[r] // k of A (codes [T, K], scales [ceil(K/128), T]).  Returns [R_cap, N]
     for row_to_tk of R_cap entries."""
-    T, K, E, N = _fp8_operands(a_codes, a_scales, expert_offsets, w_codes, w_scales)
-    _req(row_to_tk, "row_to_tk", _I32T)
+    dev, T, K, E, N = _fp8_operands(a_codes, a_scales, expert_offsets, w_codes, w_scales)
+    _arg(row_to_tk, "row_to_tk", _I32T, dev)
     R_cap = row_to_tk.numel()
-    c, code = _out(c, out_dtype, (R_cap, N), a_codes)
-    _same_device(a_codes, a_scales=a_scales, row_to_tk=row_to_tk, expert_offsets=expert_offsets, w_codes=w_codes,
-                 w_scales=w_scales, c=c)
-    _call("fp8_grouped_gemm_gather", a_codes, _ptr(a_codes), _ptr(a_scales), T, _ptr(row_to_tk), k,
-          _ptr(expert_offsets), E, R_cap, _ptr(w_codes), _ptr(w_scales), N, K, _ptr(c), code)
+    dt, dtypes, code = _out_dtype(c, out_dtype)
+    c = _give(c, "c", (R_cap, N), dt, dtypes, a_codes, dev)
+    _call("fp8_grouped_gemm_gather", dev, a_codes.data_ptr(), a_scales.data_ptr(), T, row_to_tk.data_ptr(), k,
+          expert_offsets.data_ptr(), E, R_cap, w_codes.data_ptr(), w_scales.data_ptr(), N, K, c.data_ptr(), code)
     return c
 
 
@@ -732,26 +743,36 @@ def bf16_grouped_gemm_wgrad(g, x, expert_offsets, row_to_tk=None, k: int = 1, ga
     float32 (default) or bfloat16.  g bf16 [rows, M], x bf16 [rows, N], in the expert-grouped
     order, or with gather="g" / "x" / "both" in token order: routed row r is row
     row_to_tk[r] // k of that operand."""
-    _req(g, "g", _BF16, 2)
-    _req(x, "x", _BF16, 2)
-    _req(expert_offsets, "expert_offsets", _I32T)
-    _req(row_to_tk, "row_to_tk", _I32T)
-    if gather not in (None, "g", "x", "both"):
-        raise ValueError('gather must be None, "g", "x" or "both"')
-    g_k, x_k = (k if gather in (name, "both") else 0 for name in ("g", "x"))
-    if gather is not None and (row_to_tk is None or k < 1):
-        raise ValueError("gather needs row_to_tk and k >= 1")
-    rows = [t.shape[0] for t, tk in ((g, g_k), (x, x_k)) if not tk]
-    if len(rows) == 2 and rows[0] != rows[1]:
-        raise ValueError("g and x must have the same rows")
-    R_cap = row_to_tk.numel() if gather is not None else rows[0]
-    if rows and rows[0] < R_cap:
-        raise ValueError(f"the expert-grouped operand has {rows[0]} rows, row_to_tk {R_cap} entries")
-    M, N, E = g.shape[1], x.shape[1], expert_offsets.numel() - 1
-    c, code = _out(c, out_dtype, (E, M, N), g)
-    _same_device(g, x=x, expert_offsets=expert_offsets, row_to_tk=row_to_tk, c=c)
-    _call("bf16_grouped_gemm_wgrad", g, _ptr(g), g.shape[0], g_k, _ptr(x), x.shape[0], x_k, _ptr(row_to_tk),
-          _ptr(expert_offsets), E, R_cap, M, N, _ptr(c), code)
+    dev = _head(g, "g", _BF16, 2)
+    _arg(x, "x", _BF16, dev, 2)
+    _arg(expert_offsets, "expert_offsets", _I32T, dev)
+    g_rows, M = g.shape
+    x_rows, N = x.shape
+    g_k = x_k = 0
+    if gather is None:
+        if g_rows != x_rows:
+            raise ValueError("g and x must have the same rows")
+        R_cap = g_rows
+    else:
+        if gather not in ("g", "x", "both"):
+            raise ValueError('gather must be None, "g", "x" or "both"')
+        if row_to_tk is None or k < 1:
+            raise ValueError("gather needs row_to_tk and k >= 1")
+        _arg(row_to_tk, "row_to_tk", _I32T, dev)
+        R_cap = row_to_tk.numel()
+        if gather != "x":
+            g_k = k
+        if gather != "g":
+            x_k = k
+        if gather != "both":
+            rows = x_rows if g_k else g_rows
+            if rows < R_cap:
+                raise ValueError(f"the expert-grouped operand has {rows} rows, row_to_tk {R_cap} entries")
+    E = expert_offsets.numel() - 1
+    dt, dtypes, code = _out_dtype(c, out_dtype)
+    c = _give(c, "c", (E, M, N), dt, dtypes, g, dev)
+    _call("bf16_grouped_gemm_wgrad", dev, g.data_ptr(), g_rows, g_k, x.data_ptr(), x_rows, x_k,
+          _ptr(row_to_tk) if gather else None, expert_offsets.data_ptr(), E, R_cap, M, N, c.data_ptr(), code)
     return c
 
 

@@ -564,101 +564,173 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
 }
 
 // ------------------------------------------------------------------ few rows per expert
-// A wavefront computes 16 rows x 16 columns over the whole of K by itself (so the
-// blocks add up in the order of the other kernel), a workgroup 16 rows x 64
-// columns.  Weights, activations and scales go straight into registers; the
-// loads of kAhead blocks are issued before the first is used, 2 KiB of weights
-// per wavefront and block.
-constexpr int kRowsWaves = 4, kRowsN = 16 * kRowsWaves, kRowsH = 16, kAhead = 8;
+// A workgroup takes 16 rows x 64 G columns, a wavefront G groups of 16 columns over the
+// whole of K by itself (so the blocks add up in the order of the other kernel).  The
+// weights go straight into registers, kAhead blocks of 2 KiB a wavefront ahead of
+// their use; the 16 activation rows, which every wavefront needs, and all scales
+// pass through LDS, kChunk blocks of K at a time.  More groups a wavefront read the
+// activations fewer times; fewer spread few tiles over more workgroups.
+constexpr int kRowsWaves = 4, kRowsH = 16, kAhead = 8, kChunk = 16;
 
-template <bool BF16OUT>
+// inclusive sum over the lanes up to this one
+__device__ __forceinline__ int lane_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);    // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row 0's sum to row 1, row 2's to row 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // rows 0 and 1's to rows 2 and 3
+  return v;
+}
+
+// The expert and rows of m-tile tm (16 rows each, expert by expert); e < 0 past the last.
+__device__ __forceinline__ void find_rows(const int32_t* __restrict__ offsets, int E, int Rc, int tm, int& e,
+                                          int& m0, int& rows) {
+  const int lane = lane_id();
+  int before = 0;
+  e = -1;
+  for (int e0 = 0; e0 < E && e < 0; e0 += 4 * kWave) {
+    int o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = off_at(offsets, Rc, min(e0 + q * kWave + lane, E));
+    const int over = off_at(offsets, Rc, min(e0 + 4 * kWave, E));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (e >= 0) continue;
+      const int next = q < 3 ? __builtin_amdgcn_readfirstlane(o[q < 3 ? q + 1 : q]) : over;
+      int o1 = __shfl_down(o[q], 1, kWave);
+      o1 = lane == kWave - 1 ? next : o1;
+      const int nt = max(0, o1 - o[q] + kRowsH - 1) / kRowsH;
+      const int incl = lane_scan(nt) + before;
+      const uint64_t hit = __ballot(incl > tm);
+      if (hit) {
+        const int at = __ffsll((unsigned long long)hit) - 1;
+        e = e0 + q * kWave + at;
+        const int r0 = __builtin_amdgcn_readlane(o[q], at), first = __builtin_amdgcn_readlane(incl - nt, at);
+        m0 = r0 + (tm - first) * kRowsH;
+        rows = min(kRowsH, __builtin_amdgcn_readlane(o1, at) - m0);
+      }
+      before = __builtin_amdgcn_readlane(incl, kWave - 1);
+    }
+  }
+}
+
+template <bool BF16OUT, int G>
 __global__ __launch_bounds__(kRowsWaves * 64)
 void rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, int a_rows,
                  const int32_t* __restrict__ a_map, int a_div, const int32_t* __restrict__ offsets, int E,
                  int Rc, const uint8_t* __restrict__ w, const float* __restrict__ sw, int N, int K,
                  void* __restrict__ c) {
   constexpr bool F16 = !BF16OUT;
-  const int lane = lane_id(), l16 = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int tm = blockIdx.y, n0 = (blockIdx.x * kRowsWaves + wave) * 16;
-  if (n0 >= N) return;
-
-  // the expert of m-tile tm: every wavefront scans the experts, 64 at a time
-  int e = -1, m0 = 0, rows = 0, before = 0;
-  for (int e0 = 0; e0 < E && e < 0; e0 += kWave) {
-    const int x = e0 + lane;
-    const int o0 = x < E ? off_at(offsets, Rc, x) : 0, o1 = x < E ? off_at(offsets, Rc, x + 1) : 0;
-    const int nt = max(0, o1 - o0 + kRowsH - 1) / kRowsH;
-    int incl = nt;
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      const int y = __shfl_up(incl, off, kWave);
-      if (lane >= off) incl += y;
-    }
-    incl += before;
-    const uint64_t hit = __ballot(incl > tm);
-    if (hit) {
-      const int at = __ffsll((unsigned long long)hit) - 1;
-      const int first = __shfl(incl - nt, at, kWave), r0 = __shfl(o0, at, kWave), r1 = __shfl(o1, at, kWave);
-      e = e0 + at;
-      m0 = r0 + (tm - first) * kRowsH;
-      rows = min(kRowsH, r1 - m0);
-    }
-    before = __shfl(incl, kWave - 1, kWave);
-  }
+  constexpr int kCols = 16 * kRowsWaves * G, kNb = (kCols + BK - 1) / BK;
+  // block kb of row r: 8 chunks of 16 bytes, chunk ch at ch ^ (r / 2 mod 8) (conflict-free
+  // fragment reads, see the other kernel)
+  __shared__ __align__(16) uint8_t as[kChunk][kRowsH * BK];
+  __shared__ float sas[kChunk][kRowsH];
+  __shared__ float sws[kNb][kChunk];
+  const int tid = threadIdx.x, lane = lane_id(), l16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int e, m0 = 0, rows = 0;
+  find_rows(offsets, E, Rc, blockIdx.y, e, m0, rows);
   if (e < 0) return;
-  e = __builtin_amdgcn_readfirstlane(e);
-  m0 = __builtin_amdgcn_readfirstlane(m0);
-  rows = __builtin_amdgcn_readfirstlane(rows);
-
+  const int n_wg = blockIdx.x * kCols, n0 = n_wg + 16 * G * wave;
   const int nk = (K + BK - 1) / BK, nnb = (N + BK - 1) / BK;
-  int m = m0 + min(l16, rows - 1);
-  if (a_map) m = min(max(a_map[m], 0) / a_div, a_rows - 1);
-  const uint8_t* pa = a + (int64_t)m * K;
-  const uint8_t* pw = w + ((int64_t)e * N + min(n0 + l16, N - 1)) * K;
-  const float* psa = sa + m;
-  const float* psw = sw + ((int64_t)e * nnb + n0 / BK) * nk;   // 16 columns lie in one block
 
-  // chunks g and g + 4 of block kb of a row; chunks past K are zero
+  // columns past N read the last one (never stored), chunks past K are zero
+  const uint8_t* pw[G];
+#pragma unroll
+  for (int q = 0; q < G; ++q) pw[q] = w + ((int64_t)e * N + min(n0 + 16 * q + l16, N - 1)) * K;
   auto load = [&](const uint8_t* row, int kb) __attribute__((always_inline)) -> v8i {
     const int k = kb * BK + 16 * g;
     const v4i z = {0, 0, 0, 0};
     return join(k < K ? *reinterpret_cast<const v4i*>(row + k) : z,
                 k + 64 < K ? *reinterpret_cast<const v4i*>(row + k + 64) : z);
   };
-  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  auto chunk = [&](int kb0, auto full) __attribute__((always_inline)) {
-    v8i wv[kAhead], av[kAhead];
-    float ss[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (full || kb0 + u < nk) {
-        wv[u] = load(pw, kb0 + u);
-        av[u] = load(pa, kb0 + u);
-        ss[u] = psa[(int64_t)(kb0 + u) * a_rows] * psw[kb0 + u];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (full || kb0 + u < nk) {
-        const floatx4 p = block_sum(Frag<F16>(wv[u]), Frag<F16>(av[u]));
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(p[v], ss[u], acc[v]);
-      }
-    }
-  };
-  int kb = 0;
-  for (; kb + kAhead <= nk; kb += kAhead) chunk(kb, std::true_type{});
-  if (kb < nk) chunk(kb, std::false_type{});
+  // thread -> activation row tid / 16 (the staging below), and its source row
+  int m = m0 + min(tid >> 4, rows - 1);
+  if (a_map) m = min(max(a_map[m], 0) / a_div, a_rows - 1);
+  const uint8_t* pa = a + (int64_t)m * K;
 
-  const int n = n0 + 4 * g;
-  if (l16 >= rows) return;
-  const int64_t at = (int64_t)(m0 + l16) * N + n;
+  floatx4 acc[G];
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    if (n + x >= N) break;
-    if constexpr (BF16OUT) static_cast<uint16_t*>(c)[at + x] = (uint16_t)bf16x2_rne(acc[x], 0.0f);
-    else static_cast<float*>(c)[at + x] = acc[x];
+  for (int q = 0; q < G; ++q) acc[q] = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < nk; k0 += kChunk) {
+    const int nc = min(kChunk, nk - k0), items = G * nc;
+    // items: the chunk's blocks of group 0, then of group 1, ..
+    v8i wv[kAhead];
+    int lq = 0, lk = 0, left = items;   // the next item to load
+    auto fetch = [&](v8i& o) __attribute__((always_inline)) {
+      if (left-- <= 0) return;
+      const uint8_t* row = pw[0];
+#pragma unroll
+      for (int q = 1; q < G; ++q) row = lq == q ? pw[q] : row;
+      o = load(row, k0 + lk);
+      if (++lk == nc) {
+        lk = 0;
+        ++lq;
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch(wv[u]);
+    // stage the chunk: thread (row r, lane t of 16) takes chunks t, t + 16, .. of row r
+    if (k0) __syncthreads();
+    const int r = tid >> 4, t = tid & 15;
+    for (int i = t; i < nc * 8; i += 16) {
+      const int kb = i >> 3, ch = i & 7, k = (k0 + kb) * BK + 16 * ch;
+      const v4i z = {0, 0, 0, 0};
+      *reinterpret_cast<v4i*>(as[kb] + r * BK + 16 * (ch ^ ((r >> 1) & 7))) =
+          k < K ? *reinterpret_cast<const v4i*>(pa + k) : z;
+    }
+    if (t < nc) sas[t][r] = sa[(int64_t)(k0 + t) * a_rows + m];
+    if (tid < kNb * kChunk) {
+      const int b = tid / kChunk, kb = tid % kChunk;
+      if (kb < nc) sws[b][kb] = sw[((int64_t)e * nnb + min(n_wg / BK + b, nnb - 1)) * nk + k0 + kb];
+    }
+    __syncthreads();
+    int q = 0, kb = 0;
+    for (int it = 0; it < items; it += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (it + u < items) {
+          const uint8_t* arow = as[kb] + l16 * BK;
+          const v8i av = join(*reinterpret_cast<const v4i*>(arow + 16 * (g ^ (l16 >> 1))),
+                              *reinterpret_cast<const v4i*>(arow + 16 * ((g + 4) ^ (l16 >> 1))));
+          const float s = sas[kb][l16] * sws[(n0 + 16 * q) / BK - n_wg / BK][kb];
+          const floatx4 p = block_sum(Frag<F16>(wv[u]), Frag<F16>(av));
+          fetch(wv[u]);
+#pragma unroll
+          for (int x = 0; x < G; ++x)
+            if (q == x) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[x][v] = __builtin_fmaf(p[v], s, acc[x][v]);
+            }
+          if (++kb == nc) {
+            kb = 0;
+            ++q;
+          }
+        }
+      }
+    }
+  }
+
+  if (l16 >= rows) return;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int n = n0 + 16 * q + 4 * g;
+    const int64_t at = (int64_t)(m0 + l16) * N + n;
+    if (n + 3 < N && (N & 3) == 0) {
+      if constexpr (BF16OUT)
+        *reinterpret_cast<v2u*>(static_cast<uint16_t*>(c) + at) = v2u{bf16x2_rne(acc[q][0], acc[q][1]), bf16x2_rne(acc[q][2], acc[q][3])};
+      else
+        *reinterpret_cast<floatx4*>(static_cast<float*>(c) + at) = acc[q];
+      continue;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (n + x >= N) break;
+      if constexpr (BF16OUT) static_cast<uint16_t*>(c)[at + x] = (uint16_t)bf16x2_rne(acc[q][x], 0.0f);
+      else static_cast<float*>(c)[at + x] = acc[q][x];
+    }
   }
 }
 
@@ -686,12 +758,24 @@ int launch(const uint8_t* a, const float* sa, int64_t a_rows, const int32_t* a_m
   const bool bf = c_dtype == NVFP4_OUT_BF16;
 #define FP8_GEMM(KERNEL, GRID, THREADS) \
   KERNEL<<<GRID, THREADS, 0, s>>>(a, sa, (int)a_rows, a_map, a_div, offsets, E, (int)R_cap, w, sw, (int)N, (int)K, c)
-  if (R_cap <= 16 * (int64_t)E || R_cap <= 64) {
+#ifndef WIDE_TILES
+#define WIDE_TILES 1024
+#endif
+#ifndef ROWS_AVG
+#define ROWS_AVG 16
+#endif
+  constexpr int64_t kWideTiles = WIDE_TILES;
+  if (R_cap <= ROWS_AVG * (int64_t)E || R_cap <= 64) {
     // sum of ceil(rows / 16) over the experts is at most this
     const int64_t mt = std::min(R_cap, R_cap / g8::kRowsH + E);
-    const dim3 grid((unsigned)((N + g8::kRowsN - 1) / g8::kRowsN), (unsigned)mt);
-    if (bf) FP8_GEMM(g8::rows_kernel<true>, grid, g8::kRowsWaves * 64);
-    else FP8_GEMM(g8::rows_kernel<false>, grid, g8::kRowsWaves * 64);
+    // four column groups a wavefront once that still gives four workgroups per CU
+    const bool wide = mt * ((N + 255) / 256) >= kWideTiles;
+    const int64_t cols = 16 * g8::kRowsWaves * (wide ? 4 : 1);
+    const dim3 grid((unsigned)((N + cols - 1) / cols), (unsigned)mt);
+    if (bf && wide) FP8_GEMM((g8::rows_kernel<true, 4>), grid, g8::kRowsWaves * 64);
+    else if (bf) FP8_GEMM((g8::rows_kernel<true, 1>), grid, g8::kRowsWaves * 64);
+    else if (wide) FP8_GEMM((g8::rows_kernel<false, 4>), grid, g8::kRowsWaves * 64);
+    else FP8_GEMM((g8::rows_kernel<false, 1>), grid, g8::kRowsWaves * 64);
     return launch_status();
   }
   const int64_t n_tiles = (N + g8::BN - 1) / g8::BN;
