@@ -84,6 +84,39 @@ def test_many_experts():
     _check(_offsets(r.integers(0, 4, 1024)), 24, 40, "bf16")
 
 
+@pytest.mark.parametrize("counts", [[0, 1, 33, 1024, 1025, 0, 0, 2100, 64, 31, 5, 96, 0, 0, 3, 700],
+                                    [1040] + [0] * 200 + [1] * 55, [40] * 4 + [0] + [2060]])
+@pytest.mark.parametrize("M,N", [(1016, 1000), (136, 264), (776, 2056)])
+@pytest.mark.parametrize("out,gather", [("f32", None), ("f32", "both"), ("bf16", "x"), ("bf16", "g")])
+def test_many_tiles(counts, M, N, out, gather):
+    """More tiles than CUs, of every kind in one launch: no rows, one, whole K-steps and a row more, more rows
+    than are mapped at a time; output sizes that end inside a tile either way."""
+    print(f"[bf16 wgrad] {len(counts)} experts {M}x{N} {out} {gather}", flush=True)
+    off = _offsets(counts)
+    R = int(off[-1])
+    r2t = np.random.default_rng(9).permutation(R + 4).astype(np.int32)[:R]   # k = 3: some rows of T come often, some never
+    pick = sorted({0, 1, 3, 4, len(counts) - 1, int(np.argmax(counts)), len(counts) // 2})
+    _check(off, M, N, out, r2t=r2t, k=3, gather=gather, T=(R + 4 + 2) // 3, spare=3,
+           experts=[e for e in pick if e < len(counts)])
+
+
+@pytest.mark.parametrize("E", [2, 5, 7, 8, 9, 13, 16, 23])
+@pytest.mark.parametrize("M,N", [(72, 136), (264, 512), (520, 1032)])
+def test_any_number_of_experts(E, M, N):
+    """Every expert's every tile is written, however the tiles fall on the XCDs."""
+    _check(_offsets([(7 * e) % 50 for e in range(E)]), M, N, "f32")
+
+
+def test_same_sums_for_any_call():
+    """A repeated call gives the same bits: no sum depends on the order in which workgroups end."""
+    off = dev(_offsets([700, 0, 33, 1500]).astype(np.int32))
+    for M, N in ((128, 256), (1024, 256), (2048, 2048)):
+        g, x = bf16_dev(W.gaussian_bf16((2233, M), 0.5, 1, 1)), bf16_dev(W.activations(2233, N, 1, 2))
+        a = host(pmg.bf16_grouped_gemm_wgrad(g, x, off))
+        for _ in range(3):
+            assert np.array_equal(a, host(pmg.bf16_grouped_gemm_wgrad(g, x, off)))
+
+
 def test_infinities_and_nan_stay_in_their_columns():
     """A value next to an expert's last row reaches only what it multiplies: the padding of a K-step adds nothing."""
     off = _offsets([5, 33])
