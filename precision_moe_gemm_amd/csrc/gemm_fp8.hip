@@ -564,13 +564,13 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
 }
 
 // ------------------------------------------------------------------ few rows per expert
-// A workgroup takes 16 rows x 64 G columns, a wavefront G groups of 16 columns over the
-// whole of K by itself (so the blocks add up in the order of the other kernel).  The
-// weights go straight into registers, kAhead blocks of 2 KiB a wavefront ahead of
-// their use; the 16 activation rows, which every wavefront needs, and all scales
-// pass through LDS, kChunk blocks of K at a time.  More groups a wavefront read the
-// activations fewer times; fewer spread few tiles over more workgroups.
+// A workgroup takes 16 rows x 64 columns, a wavefront 16 columns over the whole of K by
+// itself (so the blocks add up in the order of the other kernel).  The weights go
+// straight into registers, kAhead blocks of 2 KiB a wavefront ahead of their use; the
+// 16 activation rows, which every wavefront needs, and all scales pass through LDS,
+// kChunk blocks of K at a time.
 constexpr int kRowsWaves = 4, kRowsH = 16, kAhead = 8, kChunk = 16;
+constexpr int64_t kFewRows = 128;
 
 // inclusive sum over the lanes up to this one
 __device__ __forceinline__ int lane_scan(int v) {
@@ -615,64 +615,47 @@ __device__ __forceinline__ void find_rows(const int32_t* __restrict__ offsets, i
   }
 }
 
-template <bool BF16OUT, int G>
+template <bool BF16OUT>
 __global__ __launch_bounds__(kRowsWaves * 64)
 void rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, int a_rows,
                  const int32_t* __restrict__ a_map, int a_div, const int32_t* __restrict__ offsets, int E,
                  int Rc, const uint8_t* __restrict__ w, const float* __restrict__ sw, int N, int K,
                  void* __restrict__ c) {
   constexpr bool F16 = !BF16OUT;
-  constexpr int kCols = 16 * kRowsWaves * G, kNb = (kCols + BK - 1) / BK;
   // block kb of row r: 8 chunks of 16 bytes, chunk ch at ch ^ (r / 2 mod 8) (conflict-free
   // fragment reads, see the other kernel)
   __shared__ __align__(16) uint8_t as[kChunk][kRowsH * BK];
   __shared__ float sas[kChunk][kRowsH];
-  __shared__ float sws[kNb][kChunk];
+  __shared__ float sws[kChunk];
   const int tid = threadIdx.x, lane = lane_id(), l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int e, m0 = 0, rows = 0;
   find_rows(offsets, E, Rc, blockIdx.y, e, m0, rows);
   if (e < 0) return;
-  const int n_wg = blockIdx.x * kCols, n0 = n_wg + 16 * G * wave;
+  const int n0 = (blockIdx.x * kRowsWaves + wave) * 16;
   const int nk = (K + BK - 1) / BK, nnb = (N + BK - 1) / BK;
 
   // columns past N read the last one (never stored), chunks past K are zero
-  const uint8_t* pw[G];
-#pragma unroll
-  for (int q = 0; q < G; ++q) pw[q] = w + ((int64_t)e * N + min(n0 + 16 * q + l16, N - 1)) * K;
-  auto load = [&](const uint8_t* row, int kb) __attribute__((always_inline)) -> v8i {
+  const uint8_t* pw = w + ((int64_t)e * N + min(n0 + l16, N - 1)) * K;
+  auto load = [&](int kb) __attribute__((always_inline)) -> v8i {
     const int k = kb * BK + 16 * g;
     const v4i z = {0, 0, 0, 0};
-    return join(k < K ? *reinterpret_cast<const v4i*>(row + k) : z,
-                k + 64 < K ? *reinterpret_cast<const v4i*>(row + k + 64) : z);
+    return join(k < K ? *reinterpret_cast<const v4i*>(pw + k) : z,
+                k + 64 < K ? *reinterpret_cast<const v4i*>(pw + k + 64) : z);
   };
   // thread -> activation row tid / 16 (the staging below), and its source row
   int m = m0 + min(tid >> 4, rows - 1);
   if (a_map) m = min(max(a_map[m], 0) / a_div, a_rows - 1);
   const uint8_t* pa = a + (int64_t)m * K;
 
-  floatx4 acc[G];
-#pragma unroll
-  for (int q = 0; q < G; ++q) acc[q] = floatx4{0.f, 0.f, 0.f, 0.f};
+  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
   for (int k0 = 0; k0 < nk; k0 += kChunk) {
-    const int nc = min(kChunk, nk - k0), items = G * nc;
-    // items: the chunk's blocks of group 0, then of group 1, ..
+    const int nc = min(kChunk, nk - k0);
     v8i wv[kAhead];
-    int lq = 0, lk = 0, left = items;   // the next item to load
-    auto fetch = [&](v8i& o) __attribute__((always_inline)) {
-      if (left-- <= 0) return;
-      const uint8_t* row = pw[0];
 #pragma unroll
-      for (int q = 1; q < G; ++q) row = lq == q ? pw[q] : row;
-      o = load(row, k0 + lk);
-      if (++lk == nc) {
-        lk = 0;
-        ++lq;
-      }
-    };
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) fetch(wv[u]);
-    // stage the chunk: thread (row r, lane t of 16) takes chunks t, t + 16, .. of row r
+    for (int u = 0; u < kAhead; ++u)
+      if (u < nc) wv[u] = load(k0 + u);
+    // stage the chunk: thread (row r, t of 16) takes 16-byte chunks t, t + 16, .. of row r
     if (k0) __syncthreads();
     const int r = tid >> 4, t = tid & 15;
     for (int i = t; i < nc * 8; i += 16) {
@@ -682,55 +665,32 @@ void rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, in
           k < K ? *reinterpret_cast<const v4i*>(pa + k) : z;
     }
     if (t < nc) sas[t][r] = sa[(int64_t)(k0 + t) * a_rows + m];
-    if (tid < kNb * kChunk) {
-      const int b = tid / kChunk, kb = tid % kChunk;
-      if (kb < nc) sws[b][kb] = sw[((int64_t)e * nnb + min(n_wg / BK + b, nnb - 1)) * nk + k0 + kb];
-    }
+    // the workgroup's 64 columns lie in one block of 128
+    if (tid < nc) sws[tid] = sw[((int64_t)e * nnb + blockIdx.x * kRowsWaves * 16 / BK) * nk + k0 + tid];
     __syncthreads();
-    int q = 0, kb = 0;
-    for (int it = 0; it < items; it += kAhead) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (it + u < items) {
-          const uint8_t* arow = as[kb] + l16 * BK;
-          const v8i av = join(*reinterpret_cast<const v4i*>(arow + 16 * (g ^ (l16 >> 1))),
-                              *reinterpret_cast<const v4i*>(arow + 16 * ((g + 4) ^ (l16 >> 1))));
-          const float s = sas[kb][l16] * sws[(n0 + 16 * q) / BK - n_wg / BK][kb];
-          const floatx4 p = block_sum(Frag<F16>(wv[u]), Frag<F16>(av));
-          fetch(wv[u]);
+    for (int kb = 0; kb < kChunk; ++kb) {
+      if (kb < nc) {
+        const uint8_t* arow = as[kb] + l16 * BK;
+        const v8i av = join(*reinterpret_cast<const v4i*>(arow + 16 * (g ^ (l16 >> 1))),
+                            *reinterpret_cast<const v4i*>(arow + 16 * ((g + 4) ^ (l16 >> 1))));
+        const float s = sas[kb][l16] * sws[kb];
+        const floatx4 p = block_sum(Frag<F16>(wv[kb % kAhead]), Frag<F16>(av));
+        if (kb + kAhead < nc) wv[kb % kAhead] = load(k0 + kb + kAhead);
 #pragma unroll
-          for (int x = 0; x < G; ++x)
-            if (q == x) {
-#pragma unroll
-              for (int v = 0; v < 4; ++v) acc[x][v] = __builtin_fmaf(p[v], s, acc[x][v]);
-            }
-          if (++kb == nc) {
-            kb = 0;
-            ++q;
-          }
-        }
+        for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(p[v], s, acc[v]);
       }
     }
   }
 
+  const int n = n0 + 4 * g;
   if (l16 >= rows) return;
+  const int64_t at = (int64_t)(m0 + l16) * N + n;
 #pragma unroll
-  for (int q = 0; q < G; ++q) {
-    const int n = n0 + 16 * q + 4 * g;
-    const int64_t at = (int64_t)(m0 + l16) * N + n;
-    if (n + 3 < N && (N & 3) == 0) {
-      if constexpr (BF16OUT)
-        *reinterpret_cast<v2u*>(static_cast<uint16_t*>(c) + at) = v2u{bf16x2_rne(acc[q][0], acc[q][1]), bf16x2_rne(acc[q][2], acc[q][3])};
-      else
-        *reinterpret_cast<floatx4*>(static_cast<float*>(c) + at) = acc[q];
-      continue;
-    }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (n + x >= N) break;
-      if constexpr (BF16OUT) static_cast<uint16_t*>(c)[at + x] = (uint16_t)bf16x2_rne(acc[q][x], 0.0f);
-      else static_cast<float*>(c)[at + x] = acc[q][x];
-    }
+  for (int x = 0; x < 4; ++x) {
+    if (n + x >= N) break;
+    if constexpr (BF16OUT) static_cast<uint16_t*>(c)[at + x] = (uint16_t)bf16x2_rne(acc[x], 0.0f);
+    else static_cast<float*>(c)[at + x] = acc[x];
   }
 }
 
@@ -758,24 +718,15 @@ int launch(const uint8_t* a, const float* sa, int64_t a_rows, const int32_t* a_m
   const bool bf = c_dtype == NVFP4_OUT_BF16;
 #define FP8_GEMM(KERNEL, GRID, THREADS) \
   KERNEL<<<GRID, THREADS, 0, s>>>(a, sa, (int)a_rows, a_map, a_div, offsets, E, (int)R_cap, w, sw, (int)N, (int)K, c)
-#ifndef WIDE_TILES
-#define WIDE_TILES 1024
-#endif
-#ifndef ROWS_AVG
-#define ROWS_AVG 16
-#endif
-  constexpr int64_t kWideTiles = WIDE_TILES;
-  if (R_cap <= ROWS_AVG * (int64_t)E || R_cap <= 64) {
+  // Up to 128 rows the tiles leave CUs idle (one expert, 128 rows, 5120 x 2048: 18 us
+  // here, 23 us in tiles); from some 500 rows on 128 experts they stream the weights
+  // faster (2048 rows: 107 us here, 89 us in tiles).
+  if (R_cap <= g8::kFewRows) {
     // sum of ceil(rows / 16) over the experts is at most this
     const int64_t mt = std::min(R_cap, R_cap / g8::kRowsH + E);
-    // four column groups a wavefront once that still gives four workgroups per CU
-    const bool wide = mt * ((N + 255) / 256) >= kWideTiles;
-    const int64_t cols = 16 * g8::kRowsWaves * (wide ? 4 : 1);
-    const dim3 grid((unsigned)((N + cols - 1) / cols), (unsigned)mt);
-    if (bf && wide) FP8_GEMM((g8::rows_kernel<true, 4>), grid, g8::kRowsWaves * 64);
-    else if (bf) FP8_GEMM((g8::rows_kernel<true, 1>), grid, g8::kRowsWaves * 64);
-    else if (wide) FP8_GEMM((g8::rows_kernel<false, 4>), grid, g8::kRowsWaves * 64);
-    else FP8_GEMM((g8::rows_kernel<false, 1>), grid, g8::kRowsWaves * 64);
+    const dim3 grid((unsigned)((N + 16 * g8::kRowsWaves - 1) / (16 * g8::kRowsWaves)), (unsigned)mt);
+    if (bf) FP8_GEMM(g8::rows_kernel<true>, grid, g8::kRowsWaves * 64);
+    else FP8_GEMM(g8::rows_kernel<false>, grid, g8::kRowsWaves * 64);
     return launch_status();
   }
   const int64_t n_tiles = (N + g8::BN - 1) / g8::BN;
