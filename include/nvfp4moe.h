@@ -516,7 +516,7 @@ NVFP4MOE_API int bf16_transpose(const uint16_t* in, int64_t batches, int64_t row
  *   [E][ceil(N/128)][ceil(K/128)]; c [R_cap][N] of c_dtype (NVFP4_OUT_F32, or
  *   NVFP4_OUT_BF16: each FP32 result rounded to nearest even)
  * Rows at or past expert_offsets[E] are neither read nor written.  Malformed offsets
- * are clamped into [0, R_cap] (wrong rows, no access outside the buffers).
+ * are clamped into [0, R_cap] (wrong rows or none, no access outside the buffers).
  * Requires K % 16 == 0, 16 <= K <= FP8_MAX_K, 1 <= N <= FP8_MAX_N.
  *
  * fp8_grouped_gemm_gather - the same with the left operand gathered from token

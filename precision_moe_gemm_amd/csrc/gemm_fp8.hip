@@ -224,6 +224,7 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
         best = height(BM, q);
       }
     int carry = 0;
+    int64_t sum = 0;
     for (int e0 = 0; e0 < E; e0 += kWave) {
       const int e = e0 + lane;
       const int v = e < E ? max(0, sm.off[e + 1] - sm.off[e] + best - 1) / best : 0;
@@ -234,9 +235,13 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
         if (lane >= off) incl += y;
       }
       if (e < E) sm.tile_start[e] = carry + incl - v;
-      carry += __shfl(incl, kWave - 1, kWave);
+      const int here = __shfl(incl, kWave - 1, kWave);
+      carry += here;
+      sum += here;
     }
-    if (lane == 0) sm.tile_start[E] = carry;
+    // offsets that fall make more tiles than the rows can: no tile then, so that the
+    // tile numbers stay within the range that the host checked
+    if (lane == 0) sm.tile_start[E] = sum <= Rc / best + E ? carry : 0;
   }
   __syncthreads();
 
@@ -732,7 +737,7 @@ int launch(const uint8_t* a, const float* sa, int64_t a_rows, const int32_t* a_m
   const int64_t n_tiles = (N + g8::BN - 1) / g8::BN;
   constexpr int kFM8 = 8, kFM16 = 6;
   const int64_t max_tiles = ((R_cap + 63) / 64 + E) * n_tiles;
-  if (max_tiles > INT32_MAX) return NVFP4_ERR_SHAPE;
+  if (max_tiles > INT32_MAX - 1024) return NVFP4_ERR_SHAPE;
   int64_t grid = max_tiles < 256 ? max_tiles : 256;   // one workgroup per CU, a multiple of 8
   if (grid >= 8) grid &= ~7ll;
   if (bf && N % 8 == 0) FP8_GEMM((g8::grouped_gemm_kernel<true, true, kFM8>), (unsigned)grid, g8::kThreads);

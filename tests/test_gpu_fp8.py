@@ -284,6 +284,19 @@ def test_gemm_non_finite_values_stay_in_their_rows():
         assert np.array_equal(bits(np.delete(got, [3, 4], 0)), bits(np.delete(clean, [3, 4], 0)))
 
 
+def test_gemm_malformed_offsets_stay_inside():
+    """Falling, negative and too large offsets: rows beside the output and rows that no range names stay as they were."""
+    for R in (100, 700):
+        a, sa, w, sw = (dev(v) for v in _operands(R, 4, 80, 272, 4))
+        whole = torch.full((R + 64, 80), 5.0, device="cuda")
+        c = whole[32:32 + R]
+        for off in ([0, R, 0, R, 0], [-7, R // 2, R + 900, R, R], [R, R, R, R, R], [2 ** 31 - 1, -2 ** 31, 9, 8, 7]):
+            pmg.fp8_grouped_gemm(a, sa, dev(np.array(off, np.int32)), w, sw, c=c)
+            assert (whole[:32] == 5).all() and (whole[32 + R:] == 5).all()
+        pmg.fp8_grouped_gemm(a, sa, dev(np.array([0, 9, 9, 60, 60], np.int32)), w, sw, c=c.fill_(5))
+        assert (c[60:] == 5).all() and (c[:60] != 5).any(1).all()
+
+
 def test_gemm_repeats_bit_for_bit():
     for T in (9, 700):
         off, r2t = _routing(T, 16, 4, "zipf", 3)
