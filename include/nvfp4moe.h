@@ -469,9 +469,9 @@ NVFP4MOE_API int bf16_transpose(const uint16_t* in, int64_t batches, int64_t row
  *   weights: codes uint8 [E][N][K], scales float [E][ceil(N/128)][ceil(K/128)], one
  *            per 128 x 128 block
  *   value = e4m3(code) * scale
- * Quantisation of a block: s = amax / 448 (FP32 division), code = E4M3(x / s)
- * (FP32 quotient, nearest with ties to even, saturating at 448, sign kept; 0 if
- * s == 0).  An all-zero block has s = 0.  amax ignores NaN; a NaN has a NaN code,
+ * Quantisation of a block: s = amax / 448 (FP32 division), code = E4M3(448 x / amax),
+ * the exact quotient rounded once (nearest with ties to even, sign kept); 0 if s == 0.
+ * An all-zero block has s = 0.  amax ignores NaN; a NaN has a NaN code,
  * and a block that holds an infinity has s = inf, NaN codes for its infinities
  * and zero codes for its finite values, so either makes the products of its row NaN.
  *

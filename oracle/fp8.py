@@ -2,11 +2,14 @@
 
 TEST INFRASTRUCTURE ONLY (see ``oracle/__init__``).
 
-A block's scale is s = fl32(amax / 448); a code is E4M3(fl32(x / s)), nearest
-with ties to even, saturating at 448, the sign kept, and 0 where s == 0.  Rows
-have one scale per 128 elements ([blocks][rows]), weights one per 128 x 128
-block ([E][N blocks][K blocks]); the last block may be shorter.  The divisions
-are numpy float32 operations; everything after decoding is float64.
+A block's scale is s = fl32(amax / 448); a code is E4M3(448 x / amax), the exact
+quotient rounded once to nearest with ties to even, the sign kept, and 0 where
+s == 0.  Rows have one scale per 128 elements ([blocks][rows]), weights one per
+128 x 128 block ([E][N blocks][K blocks]); the last block may be shorter.
+
+The quotient of two float32 numbers is formed in float64.  That decides as the exact
+one does: for a midpoint b of the E4M3 grid, 448 x and b amax are integers of at most
+29 bits in common units, so an unequal pair differs by 2^-30 or more of either.
 """
 from __future__ import annotations
 
@@ -23,14 +26,13 @@ def blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
-def encode(x, s):
-    """float32 x, its block's scale s (broadcast) -> E4M3 codes uint8 (finite inputs)."""
-    x = np.asarray(x, np.float32)
-    s = np.broadcast_to(np.asarray(s, np.float32), x.shape)
-    with np.errstate(divide="ignore", invalid="ignore", over="ignore", under="ignore"):
-        q = np.where(s > 0, x / np.where(s > 0, s, np.float32(1)), np.float32(0)).astype(np.float32)
-    mag = of.e4m3_encode_nonneg(np.minimum(np.abs(q).astype(np.float64), 448.0))
-    return mag | (np.signbit(q).astype(np.uint8) << 7)
+def encode(x, amax):
+    """float32 x, its block's largest magnitude (broadcast) -> E4M3 codes uint8 (finite inputs)."""
+    x = np.asarray(x, np.float64)
+    live = np.broadcast_to(np.asarray(amax, np.float32) / MAX > 0, x.shape)
+    q = 448.0 * np.abs(x) / np.where(live, np.asarray(amax, np.float64), 1.0)
+    return np.where(live, of.e4m3_encode_nonneg(np.where(live, q, 0.0)) | (np.signbit(x).astype(np.uint8) << 7),
+                    0).astype(np.uint8)
 
 
 def quantize_rows(x):
@@ -41,8 +43,9 @@ def quantize_rows(x):
     scales = np.zeros((blocks(K), rows), np.float32)
     for j in range(blocks(K)):
         b = x[:, j * BLOCK:(j + 1) * BLOCK]
-        scales[j] = np.abs(b).max(axis=1) / MAX
-        codes[:, j * BLOCK:(j + 1) * BLOCK] = encode(b, scales[j][:, None])
+        amax = np.abs(b).max(axis=1)
+        scales[j] = amax / MAX
+        codes[:, j * BLOCK:(j + 1) * BLOCK] = encode(b, amax[:, None])
     return codes, scales
 
 
@@ -55,8 +58,9 @@ def quantize_weights(w):
     for i in range(blocks(N)):
         for j in range(blocks(K)):
             at = (slice(None), slice(i * BLOCK, (i + 1) * BLOCK), slice(j * BLOCK, (j + 1) * BLOCK))
-            scales[:, i, j] = np.abs(w[at]).max(axis=(1, 2)) / MAX
-            codes[at] = encode(w[at], scales[:, i, j][:, None, None])
+            amax = np.abs(w[at]).max(axis=(1, 2))
+            scales[:, i, j] = amax / MAX
+            codes[at] = encode(w[at], amax[:, None, None])
     return codes, scales
 
 

@@ -1,6 +1,6 @@
 // FP8 (E4M3fn) block-128 quantisers, gfx950: activation rows, expert weights in
 // both orders, and the weighted SwiGLU.  The block's scale is s = amax / 448 in
-// FP32 and a code is E4M3(x / s), nearest with ties to even.  All three are
+// FP32 and a code is E4M3(448 x / amax), nearest with ties to even.  All three are
 // bound by memory: a bf16 element moves 3 bytes in and out, an FP32 one 5.
 //
 // A 16-lane group owns one block of 128 elements, 8 per lane, so the block's
@@ -25,28 +25,51 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
-// The block's divisor: quotients x / s rounded as one IEEE division rounds
-// them.  For 2^-80 <= s <= 2^80 that is a product by y = fl(1 / s) and one
-// corrected step (q = fl(x y), e = x - q s exactly by an FMA, fl(q + e y);
-// Markstein); the E4M3 grid only looks at |q| >= 2^-10, where e is exact.
-// Outside that range (and for an infinite s) every element is divided.
-struct Divisor {
-  float s, y;
-  bool fast;
-  __device__ __forceinline__ explicit Divisor(float s_) : s(s_) {
-    fast = s_ >= 0x1p-80f && s_ <= 0x1p80f;
-    y = 1.0f / (fast ? s_ : 1.0f);
+// The quotients 448 x / amax that the codes are rounded from.  E4M3 keeps four bits,
+// so a code is the nearest one if the float handed to the conversion lies on the
+// right side of every midpoint, and on it for a tie.  For 2^-80 <= amax <= 2^80 the
+// quotient is a product by y = fl(1 / amax) and one corrected step (Markstein), which
+// rounds X / amax as one IEEE division does, X = fl(448 x):
+// - a bf16 x makes X exact, and a quotient of 8-bit numbers that is not a midpoint is
+//   2^-13 or more of itself away from one, so the rounded quotient decides;
+// - an FP32 x (ODD) leaves X a tail `lo`, and its quotient can come within 2^-30 of a
+//   midpoint: with e the sign of what the rounded quotient leaves, it is rounded to odd
+//   (towards zero, the last bit set if inexact), which no midpoint is.
+// A SwiGLU's FP32 h is itself rounded and takes the plain quotient.  Outside the range
+// (and for an infinite amax) the division is one in float64, rounded to odd as well.
+struct Ratio {
+  float a, y;
+  bool fast, zero;
+  __device__ __forceinline__ Ratio(float amax, float s) : a(amax), zero(s == 0.0f) {
+    fast = amax >= 0x1p-80f && amax <= 0x1p80f;
+    y = 1.0f / (fast ? amax : 1.0f);
   }
-  // x / s clamped to the format; a NaN stays one, s == 0 gives 0
-  __device__ __forceinline__ float operator()(float x) const {
-    float q;
+  // q > 0 nearest to a quotient that is larger by something of e's sign -> rounded to odd
+  static __device__ __forceinline__ float odd(float q, float e) {
+    const int ei = __float_as_int(e);
+    return __int_as_float((__float_as_int(q) + (ei >> 31)) | (int)min((uint32_t)ei, 1u));
+  }
+  // a NaN stays one; s == 0 gives 0
+  template <bool ODD>
+  __device__ __forceinline__ float of(float x) const {
     if (fast) {
-      q = x * y;
-      q = __builtin_fmaf(__builtin_fmaf(-q, s, x), y, q);
-    } else {
-      q = s != 0.0f ? x / s : (x != x ? x : 0.0f);
+      const float m = __builtin_fabsf(x), X = m * kMax;
+      float q = X * y;
+      if constexpr (ODD) {
+        const float lo = __builtin_fmaf(m, kMax, -X);
+        q = __builtin_fmaf(__builtin_fmaf(-q, a, X) + lo, y, q);
+        q = odd(q, __builtin_fmaf(-q, a, X) + lo);
+      } else {
+        q = __builtin_fmaf(__builtin_fmaf(-q, a, X), y, q);
+      }
+      return __builtin_copysignf(q, x);   // on magnitudes: the corrected step makes a -0 positive
     }
-    return __builtin_fabsf(q) > kMax ? __builtin_copysignf(kMax, q) : q;
+    if (x != x) return x;
+    if (zero) return 0.0f;
+    const double t = (double)kMax * (double)__builtin_fabsf(x) / (double)a;
+    const float q = (float)t;
+    const double e = t - (double)q;
+    return t != t ? (float)t : __builtin_copysignf(odd(q, e > 0.0 ? 1.0f : e < 0.0 ? -1.0f : 0.0f), x);
   }
 };
 
@@ -81,10 +104,12 @@ __device__ __forceinline__ void load_block(const void* base, int64_t at, int l, 
 }
 
 // the block's codes at `out`, in the same placement
-template <bool F32>
-__device__ __forceinline__ void store_codes(uint8_t* out, int l, int left, const float (&v)[8], const Divisor& d) {
-  const uint32_t w0 = codes4(d(v[0]), d(v[1]), d(v[2]), d(v[3]));
-  const uint32_t w1 = codes4(d(v[4]), d(v[5]), d(v[6]), d(v[7]));
+template <bool F32, bool ODD>
+__device__ __forceinline__ void store_codes(uint8_t* out, int l, int left, const float (&v)[8], const Ratio& d) {
+  float q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j] = d.of<ODD>(v[j]);
+  const uint32_t w0 = codes4(q[0], q[1], q[2], q[3]), w1 = codes4(q[4], q[5], q[6], q[7]);
   if constexpr (F32) {
     if (4 * l < left) *reinterpret_cast<uint32_t*>(out + 4 * l) = w0;
     if (64 + 4 * l < left) *reinterpret_cast<uint32_t*>(out + 64 + 4 * l) = w1;
@@ -118,8 +143,8 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
   for (int b = 0; b < NB; ++b) {
     const int k = k0 + b * kFp8Block;
     if (k >= K) break;
-    const float s = group_max(amax8(v[b])) / kMax;
-    store_codes<F32>(codes + r * K + k, l, K - k, v[b], Divisor(s));
+    const float m = group_max(amax8(v[b])), s = m / kMax;
+    store_codes<F32, F32>(codes + r * K + k, l, K - k, v[b], Ratio(m, s));
     if (l == 0) scales[(int64_t)(k / kFp8Block) * rows + r] = s;
   }
 }
@@ -176,8 +201,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_quantize_kernel(
       h[j] = silu(g[b][j]) * u[b][j];
       if (topk_w) h[j] *= w;
     }
-    const float s = group_max(amax8(h)) / kMax;
-    store_codes<F32>(codes + r * I + k, l, left, h, Divisor(s));
+    const float m = group_max(amax8(h)), s = m / kMax;
+    store_codes<F32, false>(codes + r * I + k, l, left, h, Ratio(m, s));
     if (l == 0) scales[(int64_t)(k / kFp8Block) * R_cap + r] = s;
     if (h_out) {
       uint16_t* p = h_out + r * I + k;
@@ -219,12 +244,13 @@ __global__ __launch_bounds__(kThreads) void quantize_weights_kernel(
   m = wave_max(m);
   if ((tid & (kWave - 1)) == 0) wmax[tid / kWave] = m;
   __syncthreads();
-  const float s = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])) / kMax;
-  const Divisor d(s);
+  m = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+  const float s = m / kMax;
+  const Ratio d(m, s);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = d(v[i][j]);
+    for (int j = 0; j < 8; ++j) v[i][j] = d.of<false>(v[i][j]);
   const int nn = (N + kFp8Block - 1) / kFp8Block, nk = (K + kFp8Block - 1) / kFp8Block;
   if (codes) {
     uint8_t* dst = codes + (e * N + n0) * K + k0;

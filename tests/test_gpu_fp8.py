@@ -82,6 +82,32 @@ def test_rows_ties_and_extremes():
     assert np.array_equal(got[~zero], rc[~zero]) and not (got[zero] & 0x7F).any()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_next_to_midpoints(dtype):
+    """448 x / amax at, and a few steps of x to either side of, every midpoint, for many amax and binades."""
+    r = np.random.default_rng(12)
+    pos = of.e4m3_decode(np.arange(0x7F, dtype=np.uint8))
+    mid = (pos[:-1] + pos[1:]) / 2
+    amax = np.abs(r.standard_normal(240)) * np.exp2(r.choice([-140, -100, -79, -3, 0, 5, 70, 90], 240))
+    if dtype == "bf16":
+        amax = of.bf16_to_f32(W.f32_to_bf16_bits(amax.astype(np.float32)))
+    amax = amax.astype(np.float32)
+    x = np.zeros((240, 128), np.float32)
+    x[:, :126] = amax[:, None].astype(np.float64) * mid / 448
+    for i in range(240):
+        for _ in range(i % 3):
+            x[i] = np.nextafter(x[i], np.float32(0 if i % 2 else np.inf))
+    if dtype == "bf16":
+        x = of.bf16_to_f32(W.f32_to_bf16_bits(x))
+    x = np.minimum(x, amax[:, None]) * np.where(np.arange(240) % 5 == 0, -1, 1).astype(np.float32)[:, None]
+    x[:, 127] = amax
+    codes, scales = pmg.fp8_quantize_rows(dev(x) if dtype == "f32" else bf16_dev(W.f32_to_bf16_bits(x)))
+    rc, rs = o8.quantize_rows(x)
+    assert np.array_equal(bits(host(scales)), bits(rs))
+    live = (rs > 0).T
+    assert np.array_equal(host(codes)[live[:, 0]], rc[live[:, 0]])
+
+
 def test_rows_nan_and_infinity():
     x = np.ones((3, 256), np.float32)
     x[0, 5], x[1, 7], x[2, :128] = np.nan, np.inf, np.nan

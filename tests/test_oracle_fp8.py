@@ -19,15 +19,35 @@ def _nearest(v: float) -> int:
     return at[0] if len(at) == 1 else next(i for i in at if i % 2 == 0)
 
 
-def test_codes_match_torch_and_exhaustive_search():
+def test_codes_match_exhaustive_search_and_torch():
+    """The exact quotient's nearest code; torch's conversion of the float64 quotient rounded to float32 agrees
+    wherever that is no midpoint."""
     r = np.random.default_rng(3)
     x = (r.standard_normal((16, 256)) * np.exp2(r.integers(-12, 9, (16, 256)))).astype(np.float32)
     codes, scales = o8.quantize_rows(x)
-    s = np.repeat(scales.T, 128, axis=1)
-    q = (x / s).astype(np.float32)
-    assert np.array_equal(codes, torch.from_numpy(q).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
-    for i in range(0, 256, 17):
-        assert codes[3, i] & 0x7F == _nearest(abs(float(q[3, i])))
+    amax = np.abs(x.reshape(16, 2, 128)).max(2)
+    assert np.array_equal(scales.T, amax / np.float32(448))
+    for row in (0, 3, 9):
+        for i in range(0, 256, 3):
+            want = Fraction(abs(float(x[row, i]))) * 448 / Fraction(float(amax[row, i // 128]))
+            assert codes[row, i] & 0x7F == _nearest(want) and codes[row, i] >> 7 == np.signbit(x[row, i])
+    q = (448.0 * x.astype(np.float64) / np.repeat(amax, 128, 1)).astype(np.float32)
+    mids = (E4M3_POS[:-1] + E4M3_POS[1:]) / 2
+    plain = ~np.isin(np.abs(q).astype(np.float64), mids)
+    assert np.array_equal(codes[plain], torch.from_numpy(q).to(torch.float8_e4m3fn).view(torch.uint8).numpy()[plain])
+
+
+def test_quotients_next_to_a_midpoint():
+    """448 x / amax one float32 step of x to either side of every midpoint, for amax that no power of two scales to 448."""
+    r = np.random.default_rng(4)
+    mids = (E4M3_POS[:-1] + E4M3_POS[1:]) / 2
+    for amax in np.abs(r.standard_normal(4)).astype(np.float32):
+        near = (mids * float(amax) / 448).astype(np.float32)
+        for x in (near, np.nextafter(near, np.float32(0)), np.nextafter(near, np.float32(9))):
+            x = np.minimum(x, amax)
+            got = o8.encode(x, amax)
+            for c, v in zip(got, x):
+                assert c == _nearest(Fraction(float(v)) * 448 / Fraction(float(amax)))
 
 
 def test_every_tie_goes_to_the_even_code():
