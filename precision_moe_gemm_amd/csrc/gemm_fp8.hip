@@ -20,6 +20,17 @@
 // are all that matters, straight into registers (rows_kernel).  Both form the same
 // products in the same order, so a row's bits depend neither on the kernel nor on
 // how many rows its expert has.
+//
+// Measured.  Tiles, BF16 out: 128 experts of 1536 x 2048 over 32768 gathered rows 186 us
+// (1110 TFLOP/s; 512 MB at 2.8 TB/s), one of 5120 x 2048 over 4096 rows 67 us (1280),
+// 8192^3 550 us (2000).  The grouped product is bound by the loads into LDS: with the
+// matrix instructions left out it takes 165 us, with the loads left out 137, and the
+// bytes in flight that two stages leave room for give a CU some 53 GB/s.  FP32 out:
+// 109 us (790 TFLOP/s) for the 5120 x 2048 product, 1110 us (990) for 8192^3: a SIMD's
+// two wavefronts convert, multiply and add at nearly the same time, so matrix and vector
+// cycles (1.05 and 0.9 million of 2.3) mostly add up.  Rows: one token through 8 of 128
+// experts of 1536 x 2048, 25 MB, 12 us (5 at the copy's rate; a launch and one round of
+// dependent loads).
 #include "fp8.h"
 
 #include <algorithm>
@@ -89,14 +100,16 @@ __device__ __forceinline__ int off_at(const int32_t* __restrict__ offsets, int R
 // 16 FM x 64 of it.  BM is 256 for the FP8 kernel and 192 for the FP16 one, whose
 // fragments take twice the registers.
 constexpr int BN = 256, BK = kFp8Block;
-constexpr int kTileCost = 96;                  // rows' worth of a tile's cost that does not scale with its rows
+constexpr int kTileCost = 96;                  // rows' worth of a tile's cost that does not scale with its rows:
+                                               // at 16 the grouped product takes 312 us, at 96 187, at 256 194
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int FN = 4, WN = 64;
 constexpr int kWI = BN / 8 / kWaves;           // weight load instructions per wavefront and K-step (8 rows each)
 constexpr int kWSlots = 2, kASlots = 2;        // K-steps in LDS
 constexpr uint32_t kOutOfRange = 0x80000000u;  // buffer offset that the range check drops
 
-// Tile heights to choose from: BM and the smaller multiples of 64.
+// Tile heights to choose from: BM and the smaller multiples of 64.  Against BM alone, in
+// BF16: 187 us for 193 to 204 (grouped), 67 for 75 (5120 x 2048 over 4096 rows).
 constexpr int kNumHeights = 5;
 __host__ __device__ constexpr int height(int bm, int i) { return i == 0 ? bm : 64 * ((bm - 1) / 64 + 1 - i) > 64 ? 64 * ((bm - 1) / 64 + 1 - i) : 64; }
 
@@ -154,7 +167,8 @@ struct Tile {
 
 // Tile L; `from` is an expert at or before the tile's.  An expert's tiles run in
 // groups of kGroupM m-tiles, column by column: the 32 workgroups of an XCD, on
-// consecutive tiles, then share both operands' slabs in its L2.
+// consecutive tiles, then share both operands' slabs in its L2 (8192^3: 556 us in groups
+// of 4, 575 of 1, 560 of 8).
 constexpr int kGroupM = 4;
 __device__ __forceinline__ Tile tile_at(int L, int from, int n_tiles, const int* tile_start, const int* offs, int E) {
   const int tm = L / n_tiles, lane = lane_id();
@@ -724,8 +738,8 @@ int launch(const uint8_t* a, const float* sa, int64_t a_rows, const int32_t* a_m
 #define FP8_GEMM(KERNEL, GRID, THREADS) \
   KERNEL<<<GRID, THREADS, 0, s>>>(a, sa, (int)a_rows, a_map, a_div, offsets, E, (int)R_cap, w, sw, (int)N, (int)K, c)
   // Up to 128 rows the tiles leave CUs idle (one expert, 128 rows, 5120 x 2048: 18 us
-  // here, 23 us in tiles); from some 500 rows on 128 experts they stream the weights
-  // faster (2048 rows: 107 us here, 89 us in tiles).
+  // here, 23 us in tiles; 128 experts, 128 rows: 55 and 58); from some 500 rows on 128
+  // experts they stream the weights faster (2048 rows: 107 us here, 89 us in tiles).
   if (R_cap <= g8::kFewRows) {
     // sum of ceil(rows / 16) over the experts is at most this
     const int64_t mt = std::min(R_cap, R_cap / g8::kRowsH + E);

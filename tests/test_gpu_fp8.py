@@ -119,6 +119,16 @@ def test_rows_nan_and_infinity():
         assert (codes[2, :128] & 0x7F == 0x7F).all() and scales[0, 2] == 0 and (codes[2, 128:] == 0x7E).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_long_inputs_match_short_ones(dtype):
+    """Rows of a long input, several blocks to a lane, against the same rows quantised in small calls."""
+    x = torch.randn((41000, 1040), generator=torch.Generator("cuda").manual_seed(3), device="cuda").to(dtype)
+    codes, scales = pmg.fp8_quantize_rows(x)
+    for a, b in ((0, 700), (20000, 20033), (40900, 41000)):
+        c, s = pmg.fp8_quantize_rows(x[a:b].clone())
+        assert torch.equal(codes[a:b], c) and torch.equal(scales[:, a:b], s)
+
+
 def test_rows_stop_at_the_routed_rows():
     x = dev(np.random.default_rng(1).standard_normal((40, 272)).astype(np.float32))
     off = dev(np.array([0, 3, 21], np.int32))
