@@ -14,7 +14,7 @@ def test_quantize_rows(lib):
     call = lambda **kw: f(kw.get("x", P), kw.get("dt", 0), kw.get("rows", 4), kw.get("K", 256), kw.get("off", None),
                           kw.get("E", 0), kw.get("codes", P), kw.get("scales", P), None)
     assert call(dt=2) == ERR_ARG
-    for kw in ({"K": 24}, {"K": 0}, {"K": 65552}, {"rows": -1}, {"rows": 1 << 31}, {"off": P, "E": 0}, {"off": P, "E": 1025}):
+    for kw in ({"K": 24}, {"K": 0}, {"K": 65552}, {"rows": -1}, {"rows": 1 << 28}, {"rows": 1 << 31}, {"off": P, "E": 0}, {"off": P, "E": 1025}):
         assert call(**kw) == ERR_SHAPE, kw
     for n in ("x", "codes", "scales"):
         assert call(**{n: None}) == ERR_NULL
@@ -41,7 +41,7 @@ def test_swiglu_quantize(lib):
                           kw.get("E", 4), kw.get("tw", None), kw.get("map", None), kw.get("c", P), kw.get("s", P),
                           kw.get("h", None), None)
     assert call(dt=3) == ERR_ARG
-    for kw in ({"I": 40}, {"I": 65552}, {"R": -1}, {"E": 0}, {"E": 1025}):
+    for kw in ({"I": 40}, {"I": 65552}, {"R": -1}, {"R": 1 << 28}, {"E": 0}, {"E": 1025}):
         assert call(**kw) == ERR_SHAPE, kw
     for kw in ({"gu": None}, {"off": None}, {"c": None}, {"s": None}, {"tw": P}):
         assert call(**kw) == ERR_NULL, kw

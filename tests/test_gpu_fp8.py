@@ -383,3 +383,26 @@ def test_binding_refusals():
         pmg.fp8_quantize_rows(torch.zeros(8, 20, device="cuda"))
     with pytest.raises(TypeError):
         pmg.fp8_grouped_gemm(u8, sc, off, w, sw, out_dtype=torch.float16)
+    for args in ((u8, sc, off.cpu(), w, sw), (u8, sc, off, w.cpu(), sw), (u8, sc.cpu(), off, w, sw)):
+        with pytest.raises(ValueError, match="device tensor"):
+            pmg.fp8_grouped_gemm(*args)
+    gu = torch.zeros(8, 64, device="cuda")
+    with pytest.raises(ValueError, match="row_to_tk"):
+        pmg.fp8_swiglu_quantize(gu, off, torch.zeros(8, device="cuda"))
+    with pytest.raises(ValueError, match="holds"):
+        pmg.fp8_swiglu_quantize(gu, off, torch.zeros(7, device="cuda"), torch.zeros(8, dtype=torch.int32, device="cuda"))
+
+
+def test_float8_tensors_are_codes():
+    """Codes may be held as torch.float8_e4m3fn tensors, on either side and as outputs."""
+    f8 = torch.float8_e4m3fn
+    x = dev(_values((40, 272), 2))
+    c, s = pmg.fp8_quantize_rows(x)
+    c8 = torch.empty((40, 272), dtype=f8, device="cuda")
+    got, s8 = pmg.fp8_quantize_rows(x, codes=c8)
+    assert got is c8 and torch.equal(c8.view(torch.uint8), c) and torch.equal(s8, s)
+    w, sw = pmg.fp8_quantize_weights(bf16_dev(W.gaussian_bf16((2, 48, 272), 0.02, 1, 2)))
+    off = dev(np.array([0, 9, 40], np.int32))
+    assert torch.equal(pmg.fp8_grouped_gemm(c8, s, off, w.view(f8), sw), pmg.fp8_grouped_gemm(c, s, off, w, sw))
+    ref = (c8.float() * s.t().repeat_interleave(128, 1)[:, :272])
+    assert (ref - x).abs().max() <= 2.0 ** -4 * x.abs().max() * (1 + 2.0 ** -20)
