@@ -100,6 +100,19 @@ def test_many_tiles(counts, M, N, out, gather):
            experts=[e for e in pick if e < len(counts)])
 
 
+@pytest.mark.parametrize("counts,M,N", [([0, 1, 33, 1024, 1025, 0, 2100, 64, 31, 5, 96, 3] * 4, 264, 520),
+                                        ([300, 0, 32, 1, 1500, 31, 64, 1057], 1024, 1016)])
+@pytest.mark.parametrize("out,gather", [("f32", None), ("f32", "both"), ("bf16", "x"), ("bf16", "g")])
+def test_tiles_that_would_pad_or_leave_units_idle(counts, M, N, out, gather):
+    """Outputs where 256 x 256 tiles would pad a third more, and where there are half as many of them as CUs."""
+    print(f"[bf16 wgrad] {len(counts)} experts {M}x{N} {out} {gather}", flush=True)
+    off = _offsets(counts)
+    R = int(off[-1])
+    r2t = np.random.default_rng(10).permutation(R + 4).astype(np.int32)[:R]
+    _check(off, M, N, out, r2t=r2t, k=3, gather=gather, T=(R + 6) // 3, spare=3,
+           experts=[e for e in (0, 1, 2, 3, 4, 6, 7, 25, 46) if e < len(counts)])
+
+
 @pytest.mark.parametrize("E", [2, 5, 7, 8, 9, 13, 16, 23])
 @pytest.mark.parametrize("M,N", [(72, 136), (264, 512), (520, 1032)])
 def test_any_number_of_experts(E, M, N):
