@@ -29,8 +29,9 @@
 // 109 us (790 TFLOP/s) for the 5120 x 2048 product, 1110 us (990) for 8192^3: a SIMD's
 // two wavefronts convert, multiply and add at nearly the same time, so matrix and vector
 // cycles (1.05 and 0.9 million of 2.3) mostly add up.  Rows: one token through 8 of 128
-// experts of 1536 x 2048, 25 MB, 12 us (5 at the copy's rate; a launch and one round of
-// dependent loads).
+// experts of 1536 x 2048, 25 MB, 11.6 us (5 at the copy's rate; a launch and three rounds of
+// dependent loads); 128 rows over all 128 of them, 403 MB, 49 us, the weights partly from
+// the last-level cache; 488 rows over 128 experts of 2048 x 768, FP32 out, 44 us (4.6 TB/s).
 #include "fp8.h"
 
 #include <algorithm>
@@ -134,6 +135,9 @@ static_assert(sizeof(Smem<10>) <= 160 * 1024, "LDS");
 // LDS read wait for them; the kernel waits itself (vmcnt).
 __device__ __forceinline__ void lds_dma16(const void* base, uint32_t voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void lds_dma16(const void* p, uint32_t lds) {   // each lane's own 64-bit address
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(p) : "memory", "m0");
 }
 __device__ __forceinline__ void lds_dma4(const void* base, uint32_t voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
@@ -587,9 +591,12 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
 // itself (so the blocks add up in the order of the other kernel).  The weights go
 // straight into registers, kAhead blocks of 2 KiB a wavefront ahead of their use; the
 // 16 activation rows, which every wavefront needs, and all scales pass through LDS,
-// kChunk blocks of K at a time.
-constexpr int kRowsWaves = 4, kRowsH = 16, kAhead = 8, kChunk = 16;
-constexpr int64_t kFewRows = 128;
+// kChunk blocks of K at a time, the rows by direct loads that take no registers (through
+// registers: one token through 8 experts 13.0 us for 11.6).  kAhead is 8 for BF16 outputs
+// (4: 79 us for 49, 128 rows over 128 experts of 1536 x 2048, 403 MB) and 2 for FP32 ones, where
+// the converted fragments need the registers (4: 45 us for 43, 488 rows over 128 experts of
+// 2048 x 768, 202 MB at 4.7 TB/s).
+constexpr int kRowsWaves = 4, kRowsH = 16, kChunk = 8;
 
 // inclusive sum over the lanes up to this one
 __device__ __forceinline__ int lane_scan(int v) {
@@ -641,6 +648,7 @@ void rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, in
                  int Rc, const uint8_t* __restrict__ w, const float* __restrict__ sw, int N, int K,
                  void* __restrict__ c) {
   constexpr bool F16 = !BF16OUT;
+  constexpr int kAhead = F16 ? 2 : 8;
   // block kb of row r: 8 chunks of 16 bytes, chunk ch at ch ^ (r / 2 mod 8) (conflict-free
   // fragment reads, see the other kernel)
   __shared__ __align__(16) uint8_t as[kChunk][kRowsH * BK];
@@ -662,37 +670,49 @@ void rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, in
     return join(k < K ? *reinterpret_cast<const v4i*>(pw + k) : z,
                 k + 64 < K ? *reinterpret_cast<const v4i*>(pw + k + 64) : z);
   };
-  // thread -> activation row tid / 16 (the staging below), and its source row
-  int m = m0 + min(tid >> 4, rows - 1);
-  if (a_map) m = min(max(a_map[m], 0) / a_div, a_rows - 1);
-  const uint8_t* pa = a + (int64_t)m * K;
+  // source row of the workgroup's row r
+  auto source = [&](int r) __attribute__((always_inline)) -> int {
+    const int m = m0 + min(r, rows - 1);
+    return a_map ? min(max(a_map[m], 0) / a_div, a_rows - 1) : m;
+  };
+  // Activations by direct-to-LDS loads of 1 KiB: rows 8h .. 8h+7 of a block, lane i row
+  // 8h + i / 8, physical chunk i % 8; wavefront v takes h = v % 2 of every other block.
+  // Chunks past K read the row's first of that block and are cleared in registers.
+  const int srow = 8 * (wave & 1) + (lane >> 3);
+  const int schunk = 16 * ((lane & 7) ^ ((srow >> 1) & 7));
+  const int64_t mrow = source(srow), ms = source(tid >> 4);
+  const int tail = K & (BK - 1);
 
   floatx4 acc = {0.f, 0.f, 0.f, 0.f};
   for (int k0 = 0; k0 < nk; k0 += kChunk) {
     const int nc = min(kChunk, nk - k0);
+    const int r = tid >> 4, t = tid & 15;
+    if (k0) __syncthreads();
+    const float sa_v = t < nc ? sa[(int64_t)(k0 + t) * a_rows + ms] : 0.0f;
+    // the workgroup's 64 columns lie in one block of 128
+    const float sw_v = tid < nc ? sw[((int64_t)e * nnb + blockIdx.x * kRowsWaves * 16 / BK) * nk + k0 + tid] : 0.0f;
     v8i wv[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       if (u < nc) wv[u] = load(k0 + u);
-    // stage the chunk: thread (row r, t of 16) takes 16-byte chunks t, t + 16, .. of row r
-    if (k0) __syncthreads();
-    const int r = tid >> 4, t = tid & 15;
-    for (int i = t; i < nc * 8; i += 16) {
-      const int kb = i >> 3, ch = i & 7, k = (k0 + kb) * BK + 16 * ch;
-      const v4i z = {0, 0, 0, 0};
-      *reinterpret_cast<v4i*>(as[kb] + r * BK + 16 * (ch ^ ((r >> 1) & 7))) =
-          k < K ? *reinterpret_cast<const v4i*>(pa + k) : z;
+    for (int kb = wave >> 1; kb < nc; kb += 2) {
+      const int k = (k0 + kb) * BK + schunk;
+      lds_dma16(a + mrow * K + (k < K ? k : (k0 + kb) * BK), lds_addr(as[0]) + kb * (kRowsH * BK) + (wave & 1) * 1024);
     }
-    if (t < nc) sas[t][r] = sa[(int64_t)(k0 + t) * a_rows + m];
-    // the workgroup's 64 columns lie in one block of 128
-    if (tid < nc) sws[tid] = sw[((int64_t)e * nnb + blockIdx.x * kRowsWaves * 16 / BK) * nk + k0 + tid];
+    if (t < kChunk) sas[t][r] = sa_v;
+    if (tid < kChunk) sws[tid] = sw_v;
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // the direct loads have landed (and with them the first weights)
     __syncthreads();
 #pragma unroll
     for (int kb = 0; kb < kChunk; ++kb) {
       if (kb < nc) {
         const uint8_t* arow = as[kb] + l16 * BK;
-        const v8i av = join(*reinterpret_cast<const v4i*>(arow + 16 * (g ^ (l16 >> 1))),
-                            *reinterpret_cast<const v4i*>(arow + 16 * ((g + 4) ^ (l16 >> 1))));
+        v8i av = join(*reinterpret_cast<const v4i*>(arow + 16 * (g ^ (l16 >> 1))),
+                      *reinterpret_cast<const v4i*>(arow + 16 * ((g + 4) ^ (l16 >> 1))));
+        if (tail && k0 + kb == nk - 1) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) av[x] = 16 * (g + (x & 4)) < tail ? av[x] : 0;
+        }
         const float s = sas[kb][l16] * sws[kb];
         const floatx4 p = block_sum(Frag<F16>(wv[kb % kAhead]), Frag<F16>(av));
         if (kb + kAhead < nc) wv[kb % kAhead] = load(k0 + kb + kAhead);
@@ -737,10 +757,12 @@ int launch(const uint8_t* a, const float* sa, int64_t a_rows, const int32_t* a_m
   const bool bf = c_dtype == NVFP4_OUT_BF16;
 #define FP8_GEMM(KERNEL, GRID, THREADS) \
   KERNEL<<<GRID, THREADS, 0, s>>>(a, sa, (int)a_rows, a_map, a_div, offsets, E, (int)R_cap, w, sw, (int)N, (int)K, c)
-  // Up to 128 rows the tiles leave CUs idle (one expert, 128 rows, 5120 x 2048: 18 us
-  // here, 23 us in tiles; 128 experts, 128 rows: 55 and 58); from some 500 rows on 128
-  // experts they stream the weights faster (2048 rows: 107 us here, 89 us in tiles).
-  if (R_cap <= g8::kFewRows) {
+  // Few rows per expert, and up to some 128 whatever their expert, leave tiles mostly empty
+  // or CUs idle (us here / in tiles, BF16 out: one expert of 5120 x 2048, 128 rows 19 / 23,
+  // 256 rows 26 / 23; 8 of 4096 x 2048, 192 rows 21 / 23, 256 rows 26 / 23; 128 of 1536 x 2048,
+  // 1024 rows 78 / 87, 2048 rows 100 / 91.  FP32 out, 128 of 2048 x 768: 1024 rows 47 / 52,
+  // 2048 rows 58 / 54).
+  if (R_cap <= 128 + 8 * (int64_t)E) {
     // sum of ceil(rows / 16) over the experts is at most this
     const int64_t mt = std::min(R_cap, R_cap / g8::kRowsH + E);
     const dim3 grid((unsigned)((N + 16 * g8::kRowsWaves - 1) / (16 * g8::kRowsWaves)), (unsigned)mt);

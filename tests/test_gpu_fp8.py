@@ -269,11 +269,12 @@ SMALL = [  # T, E, k, N, K, routing: few rows per expert
     (5, 8, 3, 130, 144, "zipf"), (16, 16, 4, 96, 784, "uniform"), (61, 128, 8, 256, 768, "uniform"),
     (64, 1, 1, 300, 2064, "softmax"), (200, 1024, 1, 40, 32, "zipf"), (40, 16, 6, 257, 1040, "zipf"),
     (3, 2, 1, 64, 4096, "uniform"), (17, 7, 1, 31, 8208, "uniform")]
-LARGE = [  # tiles through LDS
+LARGE = [  # more rows than 128 and 8 per expert (tiles through LDS), and next to that border
     (65, 1, 1, 256, 128, "softmax"), (257, 1, 1, 512, 256, "softmax"), (300, 2, 2, 272, 144, "uniform"),
     (700, 16, 4, 513, 784, "zipf"), (1021, 24, 4, 131, 1040, "zipf"), (300, 7, 3, 1, 16, "uniform"),
     (256, 3, 1, 255, 2064, "zipf"), (1100, 4, 2, 768, 528, "softmax"), (2048, 64, 2, 96, 96, "uniform"),
-    (129, 1, 1, 1030, 4000, "softmax")]
+    (129, 1, 1, 1030, 4000, "softmax"), (2100, 1024, 4, 40, 32, "zipf"), (137, 1, 1, 70, 272, "softmax"),
+    (136, 1, 1, 70, 272, "softmax")]
 
 
 @pytest.mark.parametrize("T,E,k,N,K,kind", SMALL + LARGE)

@@ -263,7 +263,7 @@ def test_far_experts_of_the_weights_and_the_product():
     for got, ref in zip((c, s, ct, st), last):
         assert torch.equal(got[-1], ref[0])
     del w, ct, st
-    for R in (40, 400):
+    for R in (40, 400, 600):
         a, sa = pmg.fp8_quantize_rows(_some(R, K))
         off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
         off[-1] = R
