@@ -36,7 +36,7 @@
 //   * tiles are scheduled like the NVFP4 GEMM: persistent workgroups,
 //     XCD-contiguous ranges, m-tile major, expert rows from device offsets;
 //     row groups past an expert's end are neither loaded nor multiplied.
-#include "common.h"
+#include "lds_dma.h"
 
 #include <type_traits>
 #include <utility>
@@ -59,7 +59,6 @@ constexpr int kWI = BN * kRowB / 1024 / kWaves;   // weight load instructions pe
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void lds_void;
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef short v8i16 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
@@ -95,24 +94,6 @@ __device__ __forceinline__ int swz(int r, int c) { return c ^ ((r >> 2) & 2); }
 // 2 (k % 4) term spreads the 4 rows over distinct banks, the 8 ((k / 8) % 2)
 // term moves the second group's rows to the other half of the banks.
 __device__ __forceinline__ int wswz(int k) { return (2 * (k & 3)) | (8 * ((k >> 3) & 1)); }
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// Direct-to-LDS load: each lane's 16 bytes at base + voff land at lds + 16 * lane.
-// Issued through inline assembly so that the compiler does not make every
-// later LDS read wait for it; the kernel waits itself (vmcnt).
-__device__ __forceinline__ void lds_dma16(const void* base, uint32_t voff, const uint8_t* lds) {
-  const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)lds);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(m), "v"(voff), "s"(base) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
 
 __device__ __forceinline__ void wait_vmcnt(int n) {
   // s_waitcnt vmcnt(n), n in [0, 15], with expcnt and lgkmcnt at their maxima

@@ -33,6 +33,7 @@
 // dependent loads); 128 rows over all 128 of them, 403 MB, 49 us, the weights partly from
 // the last-level cache; 488 rows over 128 experts of 2048 x 768, FP32 out, 44 us (4.6 TB/s).
 #include "fp8.h"
+#include "lds_dma.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -48,7 +49,6 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void lds_void;
 
 // An operand's fragment over one block of 128: lane (l16 = lane % 16, g = lane / 16)
 // holds 32 bytes of row l16, as read (FP8) or converted to FP16.  Which 32 of the
@@ -127,32 +127,6 @@ struct __align__(16) Smem {
   int64_t cost[kNumHeights];
 };
 static_assert(sizeof(Smem<10>) <= 160 * 1024, "LDS");
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// Direct-to-LDS loads: lane i's 16 (4) bytes at base + voff land at lds + 16 (4) i.
-// Issued through inline assembly so that the compiler does not make every later
-// LDS read wait for them; the kernel waits itself (vmcnt).
-__device__ __forceinline__ void lds_dma16(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
-}
-__device__ __forceinline__ void lds_dma16(const void* p, uint32_t lds) {   // each lane's own 64-bit address
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(p) : "memory", "m0");
-}
-__device__ __forceinline__ void lds_dma4(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)p);
-}
-
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
 
 // Waits until at most n of this wavefront's loads and stores are outstanding (or
 // fewer: n is rounded down to one of the counts below).

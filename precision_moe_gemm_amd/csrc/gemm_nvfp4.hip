@@ -56,7 +56,7 @@
 // with the same MFMAs (so the same bits) as in a whole tile, and a quarter
 // costs about three quarters of a whole tile (its loads, barriers and
 // activation decode do not shrink).
-#include "common.h"
+#include "lds_dma.h"
 
 #include <type_traits>
 
@@ -86,7 +86,6 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void lds_void;
 
 struct __align__(16) Stage {
   uint8_t a[BM * kRowB];       // 4 KiB FP4 activation codes, row-major
@@ -134,46 +133,6 @@ __device__ __forceinline__ half8 decode8(uint32_t w, uint32_t sp) {
   const half2v p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 3) * s2;
   return half8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
-
-// Workgroup barrier that orders LDS only: global memory (in particular the
-// direct-to-LDS loads still in flight) is left alone, so the barrier does not
-// wait for them; their completion is waited for explicitly with vmcnt.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// Direct-to-LDS loads (global_load_lds): each lane's 16 (or 4) bytes at
-// base + voff land at lds + 16 * lane (4 * lane).  Issued through inline
-// assembly so that the compiler, which cannot tell which LDS bytes such a load
-// writes, does not make every later LDS read wait for all of them; the kernel
-// waits for them itself (vmcnt) before the barrier that publishes a stage.
-// The compiler does not count these loads, so its own vmcnt waits for other
-// loads only become stricter.  M0 is written here and nowhere else in the
-// kernel (no other M0-using instruction is generated).
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void lds_dma16(const uint8_t* base, uint32_t voff, const uint8_t* lds) {
-  const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)lds);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(m), "v"(voff), "s"(base) : "memory", "m0");
-}
-__device__ __forceinline__ void lds_dma4(const uint8_t* base, uint32_t voff, const uint8_t* lds) {
-  const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)lds);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2"
-               :: "s"(m), "v"(voff), "s"(base) : "memory", "m0");
-}
-// the same with the LDS destination given as a wave-uniform LDS byte address
-__device__ __forceinline__ void lds_dma16_at(const uint8_t* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
-}
-__device__ __forceinline__ void lds_dma4_at(const uint8_t* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2"
-               :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 __device__ __forceinline__ void wait_vmcnt(int n) {
   // s_waitcnt with expcnt and lgkmcnt at their maxima: vmcnt(n), n in {0, 3, 4, 5}
@@ -472,10 +431,10 @@ void grouped_gemm_kernel(
     if (lL == kNoTile) return 0;
     if constexpr (KT) {
       const uint32_t ls = lds_st + (uint32_t)((uintptr_t)(lds_void*)&S - (uintptr_t)(lds_void*)&sm.st[0]);
-      lds_dma16_at(src0, (uint32_t)lk * step0 + vo0, ls + ldo0);
-      lds_dma16_at(w_codes, (uint32_t)lk * step1 + vo1, ls + ldo1);
-      if (wave < 6) lds_dma16_at(src2, (uint32_t)lk * step2 + vo2, ls + ldo2);
-      else lds_dma4_at(src2, (uint32_t)lk * step2 + vo2, ls + ldo2);
+      lds_dma16(src0, (uint32_t)lk * step0 + vo0, ls + ldo0);
+      lds_dma16(w_codes, (uint32_t)lk * step1 + vo1, ls + ldo1);
+      if (wave < 6) lds_dma16(src2, (uint32_t)lk * step2 + vo2, ls + ldo2);
+      else lds_dma4(src2, (uint32_t)lk * step2 + vo2, ls + ldo2);
       if (++lk == nkl) {
         lk = 0;
         lL = next_tile(lL);
@@ -624,14 +583,14 @@ void grouped_gemm_kernel(
   auto issue_rscales = [&](const Tile& t, int rb) __attribute__((always_inline)) {
     const uint32_t dst = lds_rs + (uint32_t)rb * (BM + BN) * 4u;
     if (wave < 2)
-      lds_dma4_at(reinterpret_cast<const uint8_t*>(a_rscales),
+      lds_dma4(reinterpret_cast<const uint8_t*>(a_rscales),
                   (uint32_t)min(t.m0 + 64 * wave + lane, t.m0 + t.rows - 1) * 4u, dst + wave * 256u);
     else if (wave < 4)
-      lds_dma16_at(reinterpret_cast<const uint8_t*>(w_rscales),
+      lds_dma16(reinterpret_cast<const uint8_t*>(w_rscales),
                    ((uint32_t)t.e * N + wcol(t, 256 * (wave - 2) + 4 * lane, N - 4)) * 4u,
                    dst + BM * 4u + (wave - 2) * 1024u);
     else if (SW && wave < 6 && w_rows)   // the router weights of the tile's rows
-      lds_dma4_at(reinterpret_cast<const uint8_t*>(w_rows),
+      lds_dma4(reinterpret_cast<const uint8_t*>(w_rows),
                   (uint32_t)min(t.m0 + 64 * (wave - 4) + lane, t.m0 + t.rows - 1) * 4u,
                   lds_rw + (uint32_t)rb * BM * 4u + (wave - 4) * 256u);
   };

@@ -21,6 +21,7 @@
 //   small  64 x 64 tiles, K split over the wavefronts: one expert of 4096 rows,
 //          1024 x 2048: 41 us (420 TFLOP/s; mid 142), latency of the K-steps.
 #include "fp8.h"
+#include "lds_dma.h"
 
 #include <algorithm>
 
@@ -32,7 +33,6 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef short v8i16 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
-typedef __attribute__((address_space(3))) void lds_void;
 
 // The mid kernel.  Tiles of 128 (m) x 256 (n), four wavefronts of 64 x 128, K-step 32 rows.
 constexpr int BM = 128, BN = 256, BK = 32;
@@ -55,21 +55,6 @@ static_assert(sizeof(Smem) <= 80 * 1024, "two workgroups per CU");
 // over distinct banks, the 8 (k / 8 % 2) term moves the second group's to the
 // other half.
 __device__ __forceinline__ int swz(int k) { return (2 * (k & 3)) | (8 * ((k >> 3) & 1)); }
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// Direct-to-LDS load of the active lanes: lane i's 16 bytes at base + voff land
-// at lds + 16 i (the kernel waits itself, see gemm_bf16.hip).
-__device__ __forceinline__ void lds_dma16(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
 
 __device__ __forceinline__ void wait_vmcnt(int n) {
   // s_waitcnt vmcnt(n) for n up to 6 (expcnt, lgkmcnt at their maxima), else vmcnt(0)
@@ -277,13 +262,6 @@ struct __align__(16) Smem {
   int off[NVFP4MOE_MAX_EXPERTS + 1];
 };
 static_assert(sizeof(Smem) <= 160 * 1024, "LDS");
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void lds_dma4(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 // at most n of this wavefront's loads and stores outstanding (or fewer: n is rounded
 // down to one of the counts below)
@@ -571,7 +549,7 @@ void grouped_wgrad_kernel(Operand G, Operand X, const int32_t* __restrict__ row_
   const uint32_t ids0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)sm.idx[wave]);
   auto issue_ids = [&](int kt, int stage) __attribute__((always_inline)) {
     if (gather && kt < nk && lane < BK)
-      big::lds_dma4(row_to_tk + r0 + kt * BK, 4 * min(lane, n_rows - 1 - kt * BK), ids0 + stage * BK * 4);
+      lds_dma4(row_to_tk + r0 + kt * BK, 4 * min(lane, n_rows - 1 - kt * BK), ids0 + stage * BK * 4);
   };
   // an instruction q holds rows 8q .. 8q+7 of an operand: lane i gives row 8q + i / 8,
   // physical chunk i % 8; rows past the expert's last are written as zeros
