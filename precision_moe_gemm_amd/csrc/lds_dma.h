@@ -18,12 +18,14 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // (vmcnt) before the barrier that publishes a stage.  The compiler does not count these
 // loads, so its own vmcnt waits only become stricter.
 //
-// Nor does it look into the assembly for the wait state that the hardware asks of the
-// program between a write of M0 and a load that takes its LDS address from it, so the
-// block holds it itself.
+// Nor does it look into the assembly for the wait states that the hardware asks of the
+// program, so the block holds them itself: one between the write of M0 and the load that
+// takes its LDS address from it, and five between a vector instruction that may have
+// written `base` just before (v_readfirstlane, v_readlane) and the load that reads it.
+// s_mov is the first of the five, s_nop 3 the other four.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-#define LDS_DMA(LOAD) "s_mov_b32 m0, %0\n\ts_nop 0\n\t" LOAD
+#define LDS_DMA(LOAD) "s_mov_b32 m0, %0\n\ts_nop 3\n\t" LOAD
 __device__ __forceinline__ void lds_dma16(const void* base, uint32_t voff, uint32_t lds) {
   asm volatile(LDS_DMA("global_load_lds_dwordx4 %1, %2") :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
 }

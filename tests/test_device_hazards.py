@@ -2,8 +2,11 @@
 
 The compiler keeps them for the instructions that it emits itself, but it does not look into
 inline assembly, through which the kernels issue their direct-to-LDS loads.  On gfx9
-an instruction that writes M0 and a load into LDS, which takes its LDS address from M0, need
-one wait state between them.
+
+* an instruction that writes M0 and a load into LDS, which takes its LDS address from M0, need
+  one wait state between them;
+* a vector instruction that writes a scalar register and a memory instruction that reads it (as
+  its base address) need five.
 
 An instruction between the two is one wait state, s_nop n is n + 1.
 """
@@ -33,6 +36,15 @@ class Instruction:
 
     def ends(self):
         return self.name in ("s_branch", "s_endpgm", "s_setpc_b64")
+
+
+def scalars(arg):
+    """The scalar registers that an operand names."""
+    m = re.match(r"s\[(\d+):(\d+)\]", arg)
+    if m:
+        return set(range(int(m[1]), int(m[2]) + 1))
+    m = re.match(r"s(\d+)\b", arg)
+    return {int(m[1])} if m else set()
 
 
 def parse(listing):
@@ -65,15 +77,18 @@ def violations(code):
     for i, x in enumerate(code):
         if not x.memory():
             continue
+        reads = set().union(*(scalars(a) for a in x.args)) if x.args else set()
         todo, seen = [(p, 0) for p in before(i)], {}
         while todo:
             p, gap = todo.pop()
-            if gap >= 1 or seen.get(p, 9) <= gap:
+            if gap >= 5 or seen.get(p, 9) <= gap:
                 continue
             seen[p] = gap
             y = code[p]
-            if x.into_lds() and y.args[:1] == ["m0"]:
+            if gap < 1 and x.into_lds() and y.args[:1] == ["m0"]:
                 found.append(("M0", y, x))
+            if y.name.startswith("v_") and y.args and scalars(y.args[0]) & reads:
+                found.append(("scalar base", y, x))
             todo += [(q, gap + y.states) for q in before(p)]
     return found
 
@@ -96,9 +111,10 @@ def code(lib, tmp_path_factory):
 
 def test_the_listing_is_understood(code):
     loads = sum(x.into_lds() for _, c in code for x in c)
-    branches = [x for _, c in code for x in c if x.name.startswith("s_cbranch")]
     assert len(code) > 20 and loads > 100
-    assert branches and all(x.target is not None for x in branches)
+    for name, c in code:
+        at = {x.addr for x in c}
+        assert all(x.target in at for x in c if x.name.startswith(("s_branch", "s_cbranch"))), name
 
 
 def test_the_check_finds_what_it_looks_for():
@@ -108,6 +124,12 @@ def test_the_check_finds_what_it_looks_for():
     load = "global_load_lds_dwordx4 v1, s[4:5]"
     assert [w for w, *_ in violations(fn("s_mov_b32 m0, s3", load))] == ["M0"]
     assert not violations(fn("s_mov_b32 m0, s3", "s_nop 0", load))
+    assert [w for w, *_ in violations(fn("v_readfirstlane_b32 s5, v2", "s_mov_b32 m0, s3", "s_nop 0", load))] == ["scalar base"]
+    assert not violations(fn("v_readfirstlane_b32 s5, v2", "s_mov_b32 m0, s3", "s_nop 3", load))
+    # through a branch: the write is far away in the listing and next to the load on the path
+    far = fn("s_nop 0", load, "s_endpgm", "s_mov_b32 m0, s3", ("s_branch 65532", " <f+0x4>"))
+    assert not violations(far)   # the branch itself is a wait state
+    assert violations(fn("s_nop 0", load, "s_endpgm", "v_cmp_eq_u32_e64 s[4:5], v0, v1", ("s_branch 65532", " <f+0x4>")))
 
 
 def _bad(code, kind):
@@ -117,4 +139,9 @@ def _bad(code, kind):
 
 def test_loads_into_lds_wait_for_m0(code):
     bad = _bad(code, "M0")
+    assert not bad, f"{len(bad)} pairs too close, e.g.\n" + "\n".join(bad[:10])
+
+
+def test_memory_instructions_wait_for_scalars_of_vector_instructions(code):
+    bad = _bad(code, "scalar base")
     assert not bad, f"{len(bad)} pairs too close, e.g.\n" + "\n".join(bad[:10])
