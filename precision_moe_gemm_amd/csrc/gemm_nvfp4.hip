@@ -65,6 +65,8 @@ namespace g5 {
 
 constexpr int BM = 128, BN = 512, BK = 64;
 constexpr int kStages = 3;
+// bases come back from vector lanes in most instantiations (see lds_dma.h)
+constexpr int kBaseWait = 3;
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
 constexpr int kRowB = BK / 2;                // 32 code bytes per row per K-step
@@ -431,10 +433,10 @@ void grouped_gemm_kernel(
     if (lL == kNoTile) return 0;
     if constexpr (KT) {
       const uint32_t ls = lds_st + (uint32_t)((uintptr_t)(lds_void*)&S - (uintptr_t)(lds_void*)&sm.st[0]);
-      lds_dma16(src0, (uint32_t)lk * step0 + vo0, ls + ldo0);
-      lds_dma16(w_codes, (uint32_t)lk * step1 + vo1, ls + ldo1);
-      if (wave < 6) lds_dma16(src2, (uint32_t)lk * step2 + vo2, ls + ldo2);
-      else lds_dma4(src2, (uint32_t)lk * step2 + vo2, ls + ldo2);
+      lds_dma16<kBaseWait>(src0, (uint32_t)lk * step0 + vo0, ls + ldo0);
+      lds_dma16<kBaseWait>(w_codes, (uint32_t)lk * step1 + vo1, ls + ldo1);
+      if (wave < 6) lds_dma16<kBaseWait>(src2, (uint32_t)lk * step2 + vo2, ls + ldo2);
+      else lds_dma4<kBaseWait>(src2, (uint32_t)lk * step2 + vo2, ls + ldo2);
       if (++lk == nkl) {
         lk = 0;
         lL = next_tile(lL);
@@ -447,14 +449,14 @@ void grouped_gemm_kernel(
 #pragma unroll
     for (int u = 0; u < kCIW; ++u) {
       const int q = wave + kWaves * u;
-      if (q < BM / 32) lds_dma16(a_codes, ka + off_c[u], S.a + q * 1024);
-      else if (q < kCI) lds_dma16(w_codes, kw + off_c[u], S.a + q * 1024);
+      if (q < BM / 32) lds_dma16<kBaseWait>(a_codes, ka + off_c[u], S.a + q * 1024);
+      else if (q < kCI) lds_dma16<kBaseWait>(w_codes, kw + off_c[u], S.a + q * 1024);
     }
 #pragma unroll
     for (int u = 0; u < kSIW; ++u) {
       const int q = wave + kWaves * u;
-      if (q < 2) lds_dma4(a_bscales, kss + off_s[u], S.as + q * 256);
-      else if (q < kSI) lds_dma4(w_bscales, kws + off_s[u], S.as + q * 256);
+      if (q < 2) lds_dma4<kBaseWait>(a_bscales, kss + off_s[u], S.as + q * 256);
+      else if (q < kSI) lds_dma4<kBaseWait>(w_bscales, kws + off_s[u], S.as + q * 256);
     }
     if (++lk == nkl) {
       lk = 0;
@@ -583,14 +585,14 @@ void grouped_gemm_kernel(
   auto issue_rscales = [&](const Tile& t, int rb) __attribute__((always_inline)) {
     const uint32_t dst = lds_rs + (uint32_t)rb * (BM + BN) * 4u;
     if (wave < 2)
-      lds_dma4(reinterpret_cast<const uint8_t*>(a_rscales),
+      lds_dma4<kBaseWait>(reinterpret_cast<const uint8_t*>(a_rscales),
                   (uint32_t)min(t.m0 + 64 * wave + lane, t.m0 + t.rows - 1) * 4u, dst + wave * 256u);
     else if (wave < 4)
-      lds_dma16(reinterpret_cast<const uint8_t*>(w_rscales),
+      lds_dma16<kBaseWait>(reinterpret_cast<const uint8_t*>(w_rscales),
                    ((uint32_t)t.e * N + wcol(t, 256 * (wave - 2) + 4 * lane, N - 4)) * 4u,
                    dst + BM * 4u + (wave - 2) * 1024u);
     else if (SW && wave < 6 && w_rows)   // the router weights of the tile's rows
-      lds_dma4(reinterpret_cast<const uint8_t*>(w_rows),
+      lds_dma4<kBaseWait>(reinterpret_cast<const uint8_t*>(w_rows),
                   (uint32_t)min(t.m0 + 64 * (wave - 4) + lane, t.m0 + t.rows - 1) * 4u,
                   lds_rw + (uint32_t)rb * BM * 4u + (wave - 4) * 256u);
   };

@@ -19,29 +19,36 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // loads, so its own vmcnt waits only become stricter.
 //
 // Nor does it look into the assembly for the wait states that the hardware asks of the
-// program, so the block holds them itself: one between the write of M0 and the load that
-// takes its LDS address from it, and five between a vector instruction that may have
-// written `base` just before (v_readfirstlane, v_readlane) and the load that reads it.
-// s_mov is the first of the five, s_nop 3 the other four.
+// program, so the block holds them itself.  The load comes one state after the write of M0,
+// from which it takes its LDS address.  It comes five states after a vector instruction that
+// writes a scalar register of `base`: where the compiler runs out of scalar registers and
+// reads bases back from lanes of a vector register (v_readlane), the caller asks for NOP = 3,
+// which with s_mov makes five.  Elsewhere NOP is 0; a test of the built code looks for vector
+// writes that come too close.  (Five states everywhere: 1158 us for 1104 in the FP8 product
+// of 8192^3 with FP32 outputs, 1 to 3 % in the others; nothing in the NVFP4 products.)
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-#define LDS_DMA(LOAD) "s_mov_b32 m0, %0\n\ts_nop 3\n\t" LOAD
+template <int NOP = 0>
 __device__ __forceinline__ void lds_dma16(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile(LDS_DMA("global_load_lds_dwordx4 %1, %2") :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop %3\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(lds), "v"(voff), "s"(base), "n"(NOP) : "memory", "m0");
 }
+template <int NOP = 0>
 __device__ __forceinline__ void lds_dma4(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile(LDS_DMA("global_load_lds_dword %1, %2") :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop %3\n\tglobal_load_lds_dword %1, %2"
+               :: "s"(lds), "v"(voff), "s"(base), "n"(NOP) : "memory", "m0");
 }
 __device__ __forceinline__ void lds_dma16(const void* p, uint32_t lds) {   // each lane's own 64-bit address
-  asm volatile(LDS_DMA("global_load_lds_dwordx4 %1, off") :: "s"(lds), "v"(p) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(p) : "memory", "m0");
 }
-#undef LDS_DMA
 #pragma clang diagnostic pop
+template <int NOP = 0>
 __device__ __forceinline__ void lds_dma16(const void* base, uint32_t voff, const uint8_t* lds) {
-  lds_dma16(base, voff, lds_addr(lds));
+  lds_dma16<NOP>(base, voff, lds_addr(lds));
 }
+template <int NOP = 0>
 __device__ __forceinline__ void lds_dma4(const void* base, uint32_t voff, const uint8_t* lds) {
-  lds_dma4(base, voff, lds_addr(lds));
+  lds_dma4<NOP>(base, voff, lds_addr(lds));
 }
 
 // A barrier that orders LDS accesses alone: loads and stores to memory stay in flight.
