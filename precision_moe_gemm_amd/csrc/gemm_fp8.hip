@@ -90,6 +90,29 @@ __device__ __forceinline__ v8i join(v4i a, v4i b) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// A block's term is sa sw p, p its sum of code products (2^-18 <= |p| < 2^25, or 0), added as
+// fma(p, fl(sa sw), acc).  Where fl(sa sw) leaves the normal range it has lost bits or is zero or
+// infinite, while the term may be an ordinary number: then the mantissas are multiplied and the
+// exponents added, and the term is rounded once more only if it is itself below that range.
+struct Scale {
+  float s, m;
+  int e;
+  bool far;
+  __device__ __forceinline__ Scale(float sa, float sw)
+      : s(sa * sw), m(__builtin_amdgcn_frexp_mantf(sa) * __builtin_amdgcn_frexp_mantf(sw)),
+        e(__builtin_amdgcn_frexp_expf(sa) + __builtin_amdgcn_frexp_expf(sw)),
+        far(__builtin_amdgcn_classf(s, 0x2F4) && sa != 0.0f && sw != 0.0f) {}   // subnormal, zero or infinite
+  __device__ __forceinline__ float add(float p, float acc) const {
+    return far ? acc + __builtin_ldexpf(p * m, e) : __builtin_fmaf(p, s, acc);
+  }
+};
+// The sum of the two exponents, as an unsigned distance from the least one whose products are
+// all normal numbers: some product may be out of range if it is above kNear.
+constexpr uint32_t kNear = 251;
+__device__ __forceinline__ uint32_t exponents(float sa, float sw) {
+  return (uint32_t)(__builtin_amdgcn_frexp_expf(sa) + __builtin_amdgcn_frexp_expf(sw) + 124);
+}
+
 // expert offsets clamped into [0, Rc]: malformed offsets give wrong rows but no
 // access outside the buffers
 __device__ __forceinline__ int off_at(const int32_t* __restrict__ offsets, int Rc, int e) {
@@ -125,6 +148,7 @@ struct __align__(16) Smem {
   int tile_start[NVFP4MOE_MAX_EXPERTS + 1];   // first m-tile of each expert
   int off[NVFP4MOE_MAX_EXPERTS + 1];          // its first row
   int64_t cost[kNumHeights];
+  int far[kWaves];            // the wavefront met a scale product that may be out of range
 };
 static_assert(sizeof(Smem<10>) <= 160 * 1024, "LDS");
 
@@ -192,6 +216,7 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
   const int n_tiles = (N + BN - 1) / BN;
 
   for (int e = tid; e <= E; e += kThreads) sm.off[e] = off_at(offsets, Rc, e);
+  if (tid < kWaves) sm.far[tid] = 0;
   __syncthreads();
   if (wave < kNumHeights) {
     // Tile height: the candidate with the smallest estimated critical path,
@@ -382,7 +407,7 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
   // is skipped, a partial one computed whole (the stage's other rows are whatever
   // it held, their results are never stored); the next group's reads are issued
   // before this one's matrix instructions.
-  constexpr int FB = F16 || FM > 8 ? 1 : 2;
+  constexpr int FB = F16 ? 1 : 2;
   auto mma_step = [&](int slot, int nf, bool clear) __attribute__((always_inline)) {
     const uint8_t* wrow = sm.w[0] + slot * (BN * BK) + (WN * wn + l16) * BK;
     const uint8_t* arow = sm.a[0] + slot * (BM * BK) + (16 * wm + l16) * BK;
@@ -534,6 +559,10 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
   wk = ak = nk;
   begin_loads(0);
   Tile prev{0, 0, 0, 0};
+  // The largest exponents() of the wavefront's scales so far; the FP8 kernel, which has no
+  // register free, notes in LDS that it went past kNear (in a register: gate_up 234 us for 188;
+  // the FP16 kernel with the note 1150 for 1121, 8192^3).  Without the check 185 and 1105.
+  uint32_t reach = 0;
   for (int L = begin; L < end; L += step) {
     const Tile t = find(L, prev.e);
     const int nf = min(FM, (((t.rows + 15) >> 4) - wm + 1) >> 1);
@@ -551,6 +580,17 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
         }
         lds_barrier();
       }
+      // this wavefront's scale products, a row in 64 to a lane
+      float rs[(FM + 3) / 4];
+#pragma unroll
+      for (int h = 0; h < (FM + 3) / 4; ++h)
+        rs[h] = sm.sa[slot][min(16 * wm + l16 + 32 * (g + 4 * h), t.rows - 1)];
+      const float cs = sm.sw[slot][wn >> 1];
+      if constexpr (!F16) reach = 0;
+#pragma unroll
+      for (int h = 0; h < (FM + 3) / 4; ++h) reach = max(reach, exponents(rs[h], cs));
+      if constexpr (!F16)
+        if (__builtin_amdgcn_ballot_w64(reach > kNear) != 0) sm.far[wave] = 1;
       if (kt == 0) st = epilogue(prev);   // before the first tile: no rows, nothing is written
       mma_step(slot, nf, clear);
       slot ^= 1;
@@ -558,6 +598,52 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
     prev = t;
   }
   (void)epilogue(prev);
+  if (F16 ? __builtin_amdgcn_ballot_w64(reach > kNear) == 0 : sm.far[wave] == 0) return;
+
+  // Some scale product may be out of range: the wavefront goes over its tiles again and
+  // forms the 16-row groups with such a product once more, from memory, each product in the
+  // form it needs (never in practice, so it is short rather than fast).
+  wait_vmcnt(0);   // the stores of these rows above
+  int e = 0;
+  for (int L = begin; L < end; L += step) {
+    const Tile t = find(L, e);
+    e = t.e;
+    for (int r0 = 16 * wm; r0 < t.rows; r0 += 32) {
+      const int m = t.m0 + min(r0 + l16, t.rows - 1);
+      const int64_t src = a_map ? min(max(a_map[m], 0) / a_div, a_rows - 1) : m;
+      const int nb = (t.n0 + WN * wn) / BK;
+      if (nb >= nnb) break;
+      const float* psw = sw + ((int64_t)t.e * nnb + nb) * nk;
+      reach = 0;
+      for (int kb = g; kb < nk; kb += 4) reach = max(reach, exponents(sa[(int64_t)kb * a_rows + src], psw[kb]));
+      if (__builtin_amdgcn_ballot_w64(reach > kNear) == 0) continue;
+      for (int n = t.n0 + WN * wn; n < min(N, t.n0 + WN * wn + WN); n += 16) {
+        const int64_t col = (int64_t)t.e * N + min(n + l16, N - 1);
+        floatx4 r = {0.f, 0.f, 0.f, 0.f};
+        for (int kb = 0; kb < nk; ++kb) {
+          const int k = kb * BK + 16 * g;
+          auto load = [&](const uint8_t* row) __attribute__((always_inline)) -> v8i {
+            const v4i z = {0, 0, 0, 0};
+            return join(k < K ? *reinterpret_cast<const v4i*>(row + k) : z,
+                        k + 64 < K ? *reinterpret_cast<const v4i*>(row + k + 64) : z);
+          };
+          const Scale s(sa[(int64_t)kb * a_rows + src], psw[kb]);
+          const floatx4 p = block_sum(Frag<F16>(load(w + col * K)), Frag<F16>(load(a + src * K)));
+#pragma unroll
+          for (int v = 0; v < 4; ++v) r[v] = s.add(p[v], r[v]);
+        }
+        if (r0 + l16 < t.rows) {
+          const int64_t at = (int64_t)m * N + n + 4 * g;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            if (n + 4 * g + v >= N) break;
+            if constexpr (BF16OUT) static_cast<uint16_t*>(c)[at + v] = (uint16_t)bf16x2_rne(r[v], 0.0f);
+            else static_cast<float*>(c)[at + v] = r[v];
+          }
+        }
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------ few rows per expert
@@ -687,11 +773,11 @@ void rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, in
 #pragma unroll
           for (int x = 0; x < 8; ++x) av[x] = 16 * (g + (x & 4)) < tail ? av[x] : 0;
         }
-        const float s = sas[kb][l16] * sws[kb];
+        const Scale s(sas[kb][l16], sws[kb]);
         const floatx4 p = block_sum(Frag<F16>(wv[kb % kAhead]), Frag<F16>(av));
         if (kb + kAhead < nc) wv[kb % kAhead] = load(k0 + kb + kAhead);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(p[v], s, acc[v]);
+        for (int v = 0; v < 4; ++v) acc[v] = s.add(p[v], acc[v]);
       }
     }
   }
