@@ -480,7 +480,7 @@ NVFP4MOE_API int bf16_transpose(const uint16_t* in, int64_t batches, int64_t row
  *   expert_offsets: if given, only rows [0, min(expert_offsets[E], rows)) are read
  *            and written (E is unused otherwise)
  *   codes    out [rows][K]; scales out [ceil(K/128)][rows]
- * Requires K % 16 == 0, 16 <= K <= FP8_MAX_K, rows < 2^28.
+ * Requires K % 16 == 0, 16 <= K <= FP8_MAX_K, rows <= 2^28 - 16.
  *
  * fp8_quantize_weights - quantise E matrices [N][K] by 128 x 128 blocks, in the
  * stored order, transposed, or both in one pass over w:
@@ -501,7 +501,7 @@ NVFP4MOE_API int bf16_transpose(const uint16_t* in, int64_t batches, int64_t row
  *   codes [R_cap][I], scales [ceil(I/128)][R_cap]: FP8 of h
  *   h_out    bf16 bits [R_cap][I], h rounded to nearest even (NULL: not written)
  * Only rows below expert_offsets[E] are read and written.  Requires I % 16 == 0,
- * 16 <= I <= FP8_MAX_K, R_cap < 2^28.
+ * 16 <= I <= FP8_MAX_K, R_cap <= 2^28 - 16.
  *
  * fp8_grouped_gemm - grouped expert GEMM: for every expert e and row r in
  * [offsets[e], offsets[e+1]):

@@ -21,7 +21,7 @@ namespace q8 {
 
 constexpr int kRows = 16;          // rows per workgroup, one per 16-lane group
 constexpr int kThreads = 256;
-constexpr int64_t kMaxRows = int64_t(1) << 28;   // a launch holds fewer than 2^32 threads in x
+constexpr int64_t kMaxRows = (int64_t(1) << 28) - kRows;   // a launch holds fewer than 2^32 threads in x
 constexpr float kMax = 448.0f;     // largest E4M3fn value
 
 // amax of a 16-lane group
@@ -297,7 +297,7 @@ NVFP4MOE_API int fp8_quantize_rows(const void* x, int32_t x_dtype, int64_t rows,
                                    const int32_t* expert_offsets, int32_t E, uint8_t* codes,
                                    float* scales, void* stream) {
   if (x_dtype != NVFP4_IN_BF16 && x_dtype != NVFP4_IN_F32) return NVFP4_ERR_ARG;
-  if (rows < 0 || rows >= q8::kMaxRows || K <= 0 || K % 16 != 0 || K > FP8_MAX_K) return NVFP4_ERR_SHAPE;
+  if (rows < 0 || rows > q8::kMaxRows || K <= 0 || K % 16 != 0 || K > FP8_MAX_K) return NVFP4_ERR_SHAPE;
   if (expert_offsets && (E < 1 || E > NVFP4MOE_MAX_EXPERTS)) return NVFP4_ERR_SHAPE;
   if (rows == 0) return NVFP4_OK;
   if (!x || !codes || !scales) return NVFP4_ERR_NULL;
@@ -322,7 +322,7 @@ NVFP4MOE_API int fp8_swiglu_quantize(const void* gu, int32_t gu_dtype, int64_t R
                                      const int32_t* row_to_tk, uint8_t* codes, float* scales,
                                      uint16_t* h_out, void* stream) {
   if (gu_dtype != NVFP4_IN_BF16 && gu_dtype != NVFP4_IN_F32) return NVFP4_ERR_ARG;
-  if (R_cap < 0 || R_cap >= q8::kMaxRows || I <= 0 || I % 16 != 0 || I > FP8_MAX_K) return NVFP4_ERR_SHAPE;
+  if (R_cap < 0 || R_cap > q8::kMaxRows || I <= 0 || I % 16 != 0 || I > FP8_MAX_K) return NVFP4_ERR_SHAPE;
   if (E < 1 || E > NVFP4MOE_MAX_EXPERTS) return NVFP4_ERR_SHAPE;
   if (R_cap == 0) return NVFP4_OK;
   if (!gu || !expert_offsets || !codes || !scales || (topk_w && !row_to_tk)) return NVFP4_ERR_NULL;
