@@ -743,6 +743,8 @@ def bf16_grouped_gemm_wgrad(g, x, expert_offsets, row_to_tk=None, k: int = 1, ga
     float32 (default) or bfloat16.  g bf16 [rows, M], x bf16 [rows, N], in the expert-grouped
     order, or with gather="g" / "x" / "both" in token order: routed row r is row
     row_to_tk[r] // k of that operand."""
+    if gather is None and (row_to_tk is not None or k != 1):
+        raise ValueError('row_to_tk and k need gather="g", "x" or "both"')
     dev = _head(g, "g", _BF16, 2)
     _arg(x, "x", _BF16, dev, 2)
     _arg(expert_offsets, "expert_offsets", _I32T, dev)
