@@ -75,6 +75,30 @@ def test_a_row_alone_and_in_a_batch(out):
     assert torch.equal(got[300], full[300])
 
 
+@pytest.mark.parametrize("N,K", [(1032, 400), (515, 272)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_a_few_such_rows_among_many_tiles(N, K, out):
+    """One row in 50, gathered; those rows and some others as they come from the few-row kernel."""
+    T, E, k = 4000, 6, 3
+    r = np.random.default_rng(3)
+    a, sa = o8.quantize_rows(r.standard_normal((T, K)).astype(np.float32))
+    w, sw = o8.quantize_weights(r.standard_normal((E, N, K)).astype(np.float32))
+    sw[:, :, 1::2] = np.float32(2.0 ** -90)
+    far = np.arange(0, T, 50)
+    sa[:, far] = (1 + r.random((sa.shape[0], far.size))).astype(np.float32) * np.float32(2.0 ** -50)
+    expert = np.argsort(r.random((T, E)), axis=1)[:, :k].reshape(-1)
+    r2t = np.argsort(expert, kind="stable").astype(np.int32)
+    off = np.concatenate([[0], np.cumsum(np.bincount(expert, minlength=E))]).astype(np.int32)
+    full = pmg.fp8_grouped_gemm_gather(dev(a), dev(sa), dev(r2t), k, dev(off), dev(w), dev(sw), out_dtype=out)
+    assert torch.isfinite(full).all()
+    for tokens in (far[:20], far[-20:], far[:20] + 1, np.arange(1985, 2005)):
+        rows = np.nonzero(np.isin(r2t // k, tokens))[0]
+        o = np.searchsorted(rows, off).astype(np.int32)
+        assert rows.size <= 128 + 8 * E
+        got = pmg.fp8_grouped_gemm_gather(dev(a), dev(sa), dev(r2t[rows]), k, dev(o), dev(w), dev(sw), out_dtype=out)
+        assert torch.equal(got, full[torch.from_numpy(rows).cuda()])
+
+
 def test_infinite_and_nan_scales():
     """An infinite scale gives what the formula gives: an infinity, or NaN where it meets a zero."""
     one = o8.quantize_rows(np.ones((2, 128), np.float32))[0]
