@@ -50,6 +50,8 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
 
+constexpr int BK = kFp8Block;
+
 // An operand's fragment over one block of 128: lane (l16 = lane % 16, g = lane / 16)
 // holds 32 bytes of row l16, as read (FP8) or converted to FP16.  Which 32 of the
 // 128 is free as long as both operands take the same; these kernels take the
@@ -113,6 +115,30 @@ __device__ __forceinline__ uint32_t exponents(float sa, float sw) {
   return (uint32_t)(__builtin_amdgcn_frexp_expf(sa) + __builtin_amdgcn_frexp_expf(sw) + 124);
 }
 
+// The sums of 16 columns x 16 rows, from memory, each term in the form its scales call for: lane
+// (l16, g) gives column l16's weights and row l16's activations, and receives columns 4g .. 4g+3
+// of row l16.  Both kernels go back to it for rows that have met a scale product out of range
+// (never in practice, so it is short rather than fast).
+template <bool F16>
+__device__ __forceinline__ floatx4 far_sums(const uint8_t* arow, const float* sa, int a_rows, const uint8_t* wrow,
+                                            const float* sw, int nk, int K, int g) {
+  floatx4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int kb = 0; kb < nk; ++kb) {
+    const int k = kb * BK + 16 * g;
+    auto load = [&](const uint8_t* row) __attribute__((always_inline)) -> v8i {   // chunks past K are zero
+      const v4i z = {0, 0, 0, 0};
+      return join(k < K ? *reinterpret_cast<const v4i*>(row + k) : z,
+                  k + 64 < K ? *reinterpret_cast<const v4i*>(row + k + 64) : z);
+    };
+    const Scale s(sa[(int64_t)kb * a_rows], sw[kb]);
+    const floatx4 p = block_sum(Frag<F16>(load(wrow)), Frag<F16>(load(arow)));
+#pragma unroll
+    for (int v = 0; v < 4; ++v) r[v] = s.add(p[v], r[v]);
+  }
+  return r;
+}
+
 // expert offsets clamped into [0, Rc]: malformed offsets give wrong rows but no
 // access outside the buffers
 __device__ __forceinline__ int off_at(const int32_t* __restrict__ offsets, int Rc, int e) {
@@ -123,7 +149,7 @@ __device__ __forceinline__ int off_at(const int32_t* __restrict__ offsets, int R
 // A workgroup of 8 wavefronts (2 x 4) computes up to BM x 256, a wavefront up to
 // 16 FM x 64 of it.  BM is 256 for the FP8 kernel and 192 for the FP16 one, whose
 // fragments take twice the registers.
-constexpr int BN = 256, BK = kFp8Block;
+constexpr int BN = 256;
 constexpr int kTileCost = 96;                  // rows' worth of a tile's cost that does not scale with its rows:
                                                // at 16 the grouped product takes 312 us, at 96 187, at 256 194
 constexpr int kWaves = 8, kThreads = kWaves * 64;
@@ -195,6 +221,45 @@ __device__ __forceinline__ Tile tile_at(int L, int from, int n_tiles, const int*
   t.rows = max(0, min(per, o1 - t.m0));
   t.n0 = tn * BN;
   return t;
+}
+
+// The wavefront's part of its tiles once more, in the 16-row groups that have a scale product out
+// of range.  A function of its own: inlined, its live values make the tile loop spill (gate_up 241
+// us for 189).
+template <bool BF16OUT, int FM>
+__device__ __attribute__((noinline)) void far_tiles(const Smem<FM>& sm, int begin, int end, int step, const uint8_t* a,
+                                                    const float* sa, int a_rows, const int32_t* a_map, int a_div, int E,
+                                                    const uint8_t* w, const float* sw, int N, int K, void* c) {
+  const int lane = lane_id(), l16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int nk = (K + BK - 1) / BK, nnb = (N + BK - 1) / BK;
+  Tile t{0, 0, 0, 0};
+  for (int L = begin; L < end; L += step) {
+    t = tile_at(L, t.e, (N + BN - 1) / BN, sm.tile_start, sm.off, E);
+    const int nb = (t.n0 + WN * wn) / BK;
+    if (nb >= nnb) continue;
+    const float* psw = sw + ((int64_t)t.e * nnb + nb) * nk;
+    for (int r0 = 16 * wm; r0 < t.rows; r0 += 32) {
+      const int m = t.m0 + min(r0 + l16, t.rows - 1);
+      const int64_t src = a_map ? min(max(a_map[m], 0) / a_div, a_rows - 1) : m;
+      uint32_t reach = 0;
+      for (int kb = g; kb < nk; kb += 4) reach = max(reach, exponents(sa[(int64_t)kb * a_rows + src], psw[kb]));
+      if (__builtin_amdgcn_ballot_w64(reach > kNear) == 0) continue;
+      for (int n = t.n0 + WN * wn; n < min(N, t.n0 + WN * wn + WN); n += 16) {
+        const int64_t col = (int64_t)t.e * N + min(n + l16, N - 1);
+        const floatx4 r = far_sums<!BF16OUT>(a + src * K, sa + src, a_rows, w + col * K, psw, nk, K, g);
+        if (r0 + l16 >= t.rows) continue;
+        const int64_t at = (int64_t)m * N + n + 4 * g;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if (n + 4 * g + v >= N) break;
+          if constexpr (BF16OUT) static_cast<uint16_t*>(c)[at + v] = (uint16_t)bf16x2_rne(r[v], 0.0f);
+          else static_cast<float*>(c)[at + v] = r[v];
+        }
+      }
+    }
+  }
 }
 
 // WHOLE: rows of c are whole 16-byte pieces
@@ -600,50 +665,8 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
   (void)epilogue(prev);
   if (F16 ? __builtin_amdgcn_ballot_w64(reach > kNear) == 0 : sm.far[wave] == 0) return;
 
-  // Some scale product may be out of range: the wavefront goes over its tiles again and
-  // forms the 16-row groups with such a product once more, from memory, each product in the
-  // form it needs (never in practice, so it is short rather than fast).
-  wait_vmcnt(0);   // the stores of these rows above
-  int e = 0;
-  for (int L = begin; L < end; L += step) {
-    const Tile t = find(L, e);
-    e = t.e;
-    for (int r0 = 16 * wm; r0 < t.rows; r0 += 32) {
-      const int m = t.m0 + min(r0 + l16, t.rows - 1);
-      const int64_t src = a_map ? min(max(a_map[m], 0) / a_div, a_rows - 1) : m;
-      const int nb = (t.n0 + WN * wn) / BK;
-      if (nb >= nnb) break;
-      const float* psw = sw + ((int64_t)t.e * nnb + nb) * nk;
-      reach = 0;
-      for (int kb = g; kb < nk; kb += 4) reach = max(reach, exponents(sa[(int64_t)kb * a_rows + src], psw[kb]));
-      if (__builtin_amdgcn_ballot_w64(reach > kNear) == 0) continue;
-      for (int n = t.n0 + WN * wn; n < min(N, t.n0 + WN * wn + WN); n += 16) {
-        const int64_t col = (int64_t)t.e * N + min(n + l16, N - 1);
-        floatx4 r = {0.f, 0.f, 0.f, 0.f};
-        for (int kb = 0; kb < nk; ++kb) {
-          const int k = kb * BK + 16 * g;
-          auto load = [&](const uint8_t* row) __attribute__((always_inline)) -> v8i {
-            const v4i z = {0, 0, 0, 0};
-            return join(k < K ? *reinterpret_cast<const v4i*>(row + k) : z,
-                        k + 64 < K ? *reinterpret_cast<const v4i*>(row + k + 64) : z);
-          };
-          const Scale s(sa[(int64_t)kb * a_rows + src], psw[kb]);
-          const floatx4 p = block_sum(Frag<F16>(load(w + col * K)), Frag<F16>(load(a + src * K)));
-#pragma unroll
-          for (int v = 0; v < 4; ++v) r[v] = s.add(p[v], r[v]);
-        }
-        if (r0 + l16 < t.rows) {
-          const int64_t at = (int64_t)m * N + n + 4 * g;
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            if (n + 4 * g + v >= N) break;
-            if constexpr (BF16OUT) static_cast<uint16_t*>(c)[at + v] = (uint16_t)bf16x2_rne(r[v], 0.0f);
-            else static_cast<float*>(c)[at + v] = r[v];
-          }
-        }
-      }
-    }
-  }
+  wait_vmcnt(0);   // the stores of the rows that are formed once more
+  far_tiles<BF16OUT, FM>(sm, begin, end, step, a, sa, a_rows, a_map, a_div, E, w, sw, N, K, c);
 }
 
 // ------------------------------------------------------------------ few rows per expert
@@ -712,8 +735,8 @@ void rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, in
   // block kb of row r: 8 chunks of 16 bytes, chunk ch at ch ^ (r / 2 mod 8) (conflict-free
   // fragment reads, see the other kernel)
   __shared__ __align__(16) uint8_t as[kChunk][kRowsH * BK];
-  __shared__ float sas[kChunk][kRowsH];
-  __shared__ float sws[kChunk];
+  __shared__ float ss[kChunk][kRowsH];                   // products of the scales
+  __shared__ __align__(16) int fars[kRowsWaves];         // some of them may be out of range
   const int tid = threadIdx.x, lane = lane_id(), l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int e, m0 = 0, rows = 0;
@@ -741,16 +764,18 @@ void rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, in
   const int srow = 8 * (wave & 1) + (lane >> 3);
   const int schunk = 16 * ((lane & 7) ^ ((srow >> 1) & 7));
   const int64_t mrow = source(srow), ms = source(tid >> 4);
+  // the workgroup's 64 columns lie in one block of 128
+  const float* psw = sw + ((int64_t)e * nnb + blockIdx.x * kRowsWaves * 16 / BK) * nk;
   const int tail = K & (BK - 1);
 
   floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+  bool far = false;   // the wavefront staged a scale product that may be out of range
   for (int k0 = 0; k0 < nk; k0 += kChunk) {
     const int nc = min(kChunk, nk - k0);
     const int r = tid >> 4, t = tid & 15;
     if (k0) __syncthreads();
     const float sa_v = t < nc ? sa[(int64_t)(k0 + t) * a_rows + ms] : 0.0f;
-    // the workgroup's 64 columns lie in one block of 128
-    const float sw_v = tid < nc ? sw[((int64_t)e * nnb + blockIdx.x * kRowsWaves * 16 / BK) * nk + k0 + tid] : 0.0f;
+    const float sw_v = t < nc ? psw[k0 + t] : 0.0f;
     v8i wv[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
@@ -759,8 +784,9 @@ void rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, in
       const int k = (k0 + kb) * BK + schunk;
       lds_dma16(a + mrow * K + (k < K ? k : (k0 + kb) * BK), lds_addr(as[0]) + kb * (kRowsH * BK) + (wave & 1) * 1024);
     }
-    if (t < kChunk) sas[t][r] = sa_v;
-    if (tid < kChunk) sws[tid] = sw_v;
+    if (t < kChunk) ss[t][r] = sa_v * sw_v;
+    far |= __builtin_amdgcn_ballot_w64(exponents(sa_v, sw_v) > kNear) != 0;
+    fars[wave] = far;
     __builtin_amdgcn_s_waitcnt(0x0F70);   // the direct loads have landed (and with them the first weights)
     __syncthreads();
 #pragma unroll
@@ -773,15 +799,20 @@ void rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, in
 #pragma unroll
           for (int x = 0; x < 8; ++x) av[x] = 16 * (g + (x & 4)) < tail ? av[x] : 0;
         }
-        const Scale s(sas[kb][l16], sws[kb]);
+        const float sc = ss[kb][l16];
         const floatx4 p = block_sum(Frag<F16>(wv[kb % kAhead]), Frag<F16>(av));
         if (kb + kAhead < nc) wv[kb % kAhead] = load(k0 + kb + kAhead);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[v] = s.add(p[v], acc[v]);
+        for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(p[v], sc, acc[v]);
       }
     }
   }
 
+  const int4 f4 = *reinterpret_cast<const int4*>(fars);
+  if (__builtin_amdgcn_readfirstlane(f4.x | f4.y | f4.z | f4.w)) {
+    const int64_t src = source(l16);
+    acc = far_sums<F16>(a + src * K, sa + src, a_rows, pw, psw, nk, K, g);
+  }
   const int n = n0 + 4 * g;
   if (l16 >= rows) return;
   const int64_t at = (int64_t)(m0 + l16) * N + n;
