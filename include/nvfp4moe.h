@@ -471,9 +471,12 @@ NVFP4MOE_API int bf16_transpose(const uint16_t* in, int64_t batches, int64_t row
  *   value = e4m3(code) * scale
  * Quantisation of a block: s = amax / 448 (FP32 division), code = E4M3(448 x / amax),
  * the exact quotient rounded once (nearest with ties to even, sign kept); 0 if s == 0.
- * An all-zero block has s = 0.  amax ignores NaN; a NaN has a NaN code,
- * and a block that holds an infinity has s = inf, NaN codes for its infinities
- * and zero codes for its finite values, so either makes the products of its row NaN.
+ * An all-zero block has s = 0.  Where amax < 2^-117, s is below the normal range and has
+ * fewer bits, so code * s is off by more than the code's rounding (with amax = 717 * 2^-149
+ * the largest element reads as 896 * 2^-149), and with amax <= 224 * 2^-149 s is 0 and the
+ * block lost.  amax ignores NaN; a NaN has a NaN code, and a block that holds an infinity has
+ * s = inf, NaN codes for its infinities and zero codes for its finite values, so either makes
+ * the products of its row NaN.
  *
  * fp8_quantize_rows - quantise `rows` rows of length K.
  *   x        [rows][K] of x_dtype (NVFP4_IN_BF16 bits or NVFP4_IN_F32)

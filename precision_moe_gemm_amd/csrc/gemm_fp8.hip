@@ -21,17 +21,22 @@
 // products in the same order, so a row's bits depend neither on the kernel nor on
 // how many rows its expert has.
 //
-// Measured.  Tiles, BF16 out: 128 experts of 1536 x 2048 over 32768 gathered rows 186 us
-// (1110 TFLOP/s; 512 MB at 2.8 TB/s), one of 5120 x 2048 over 4096 rows 67 us (1280),
-// 8192^3 550 us (2000).  The grouped product is bound by the loads into LDS: with the
-// matrix instructions left out it takes 165 us, with the loads left out 137, and the
-// bytes in flight that two stages leave room for give a CU some 53 GB/s.  FP32 out:
-// 109 us (790 TFLOP/s) for the 5120 x 2048 product, 1110 us (990) for 8192^3: a SIMD's
-// two wavefronts convert, multiply and add at nearly the same time, so matrix and vector
-// cycles (1.05 and 0.9 million of 2.3) mostly add up.  Rows: one token through 8 of 128
-// experts of 1536 x 2048, 25 MB, 11.6 us (5 at the copy's rate; a launch and three rounds of
-// dependent loads); 128 rows over all 128 of them, 403 MB, 49 us, the weights partly from
-// the last-level cache; 488 rows over 128 experts of 2048 x 768, FP32 out, 44 us (4.6 TB/s).
+// Measured.  Tiles, BF16 out: 128 experts of 1536 x 2048 over 32768 gathered rows 187 us
+// (1100 TFLOP/s; 512 MB at 2.7 TB/s), one of 5120 x 2048 over 4096 rows 69 us (1240),
+// 8192^3 572 us (1920).  Of the grouped product's time the loads into LDS are the longer part
+// (165 us with the matrix instructions left out, 137 with the loads left out): 1.2 GB or 29
+// GB/s a CU.  A K-step's loads, some 50 KB here, where a tile holds about 136 rows, are requested
+// a step ahead and waited for in full, so no more than one step's are ever in flight.
+// FP32 out: 109 us (785 TFLOP/s) for the 5120 x 2048 product, whose 440 tiles fill the second of
+// two rounds to 72 %, 1125 us (980) for 8192^3: a SIMD's two wavefronts convert, multiply and add
+// at nearly the same time, so matrix and vector cycles (1.05 and 0.9 million of 2.3) mostly add up;
+// without the conversions it takes 7 % less, with a quarter of the FMAs 4 %.
+// The FP8 tile kernel fills its 256 registers and spills 2, the form for N not a multiple of 8
+// 21 (with 6 for the 2, gate_up took 241 us for 189).
+// Rows: one token through 8 of 128 experts of 1536 x 2048, 25 MB, 9.6 us (5 at the copy's rate; a
+// launch, then offsets, map entries, and rows and weights, each behind the one before); 128 rows
+// over all 128 of them, 403 MB, 48 us, the weights partly from the last-level cache; 488 rows over
+// 128 experts of 2048 x 768, FP32 out, 42 us (4.8 TB/s).
 #include "fp8.h"
 #include "lds_dma.h"
 
@@ -151,7 +156,8 @@ __device__ __forceinline__ int off_at(const int32_t* __restrict__ offsets, int R
 // fragments take twice the registers.
 constexpr int BN = 256;
 constexpr int kTileCost = 96;                  // rows' worth of a tile's cost that does not scale with its rows:
-                                               // at 16 the grouped product takes 312 us, at 96 187, at 256 194
+                                               // at 16 / 96 / 256 gate_up takes 313 / 189 / 199 us, the QKV product
+                                               // 108 / 70 / 70 (BF16 out), down 234 / 177 / 173, a Zipf gate_up 325 / 206 / 203
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int FN = 4, WN = 64;
 constexpr int kWI = BN / 8 / kWaves;           // weight load instructions per wavefront and K-step (8 rows each)
@@ -159,7 +165,8 @@ constexpr int kWSlots = 2, kASlots = 2;        // K-steps in LDS
 constexpr uint32_t kOutOfRange = 0x80000000u;  // buffer offset that the range check drops
 
 // Tile heights to choose from: BM and the smaller multiples of 64.  Against BM alone, in
-// BF16: 187 us for 193 to 204 (grouped), 67 for 75 (5120 x 2048 over 4096 rows).
+// BF16: 187 us for 193 to 204 (grouped), 67 for 75 (5120 x 2048 over 4096 rows), measured
+// before the check of the scale products.
 constexpr int kNumHeights = 5;
 __host__ __device__ constexpr int height(int bm, int i) { return i == 0 ? bm : 64 * ((bm - 1) / 64 + 1 - i) > 64 ? 64 * ((bm - 1) / 64 + 1 - i) : 64; }
 
@@ -625,8 +632,8 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
   begin_loads(0);
   Tile prev{0, 0, 0, 0};
   // The largest exponents() of the wavefront's scales so far; the FP8 kernel, which has no
-  // register free, notes in LDS that it went past kNear (in a register: gate_up 234 us for 188;
-  // the FP16 kernel with the note 1150 for 1121, 8192^3).  Without the check 185 and 1105.
+  // register free, notes in LDS that it went past kNear (in a register: gate_up 234 us for 187;
+  // the FP16 kernel with the note 1150 for 1125, 8192^3).  Without the check 185 and 1100.
   uint32_t reach = 0;
   for (int L = begin; L < end; L += step) {
     const Tile t = find(L, prev.e);
@@ -675,10 +682,11 @@ void grouped_gemm_kernel(const uint8_t* __restrict__ a, const float* __restrict_
 // straight into registers, kAhead blocks of 2 KiB a wavefront ahead of their use; the
 // 16 activation rows, which every wavefront needs, and all scales pass through LDS,
 // kChunk blocks of K at a time, the rows by direct loads that take no registers (through
-// registers: one token through 8 experts 13.0 us for 11.6).  kAhead is 8 for BF16 outputs
-// (4: 79 us for 49, 128 rows over 128 experts of 1536 x 2048, 403 MB) and 2 for FP32 ones, where
-// the converted fragments need the registers (4: 45 us for 43, 488 rows over 128 experts of
-// 2048 x 768, 202 MB at 4.7 TB/s).
+// registers one token through 8 experts took 12 % longer).  kAhead is 8 for BF16 outputs, so a
+// chunk's weights are all requested at its start, and none before (4: 78 us for 48, 128 rows over
+// 128 experts of 1536 x 2048, 403 MB), and 2 for FP32 ones, where the converted fragments need
+// the registers (4: 45 us for 42, 488 rows over 128 experts of 2048 x 768, 202 MB at 4.8
+// TB/s, though 11.4 for 12.5 for one token).
 constexpr int kRowsWaves = 4, kRowsH = 16, kChunk = 8;
 
 // inclusive sum over the lanes up to this one
@@ -849,9 +857,9 @@ int launch(const uint8_t* a, const float* sa, int64_t a_rows, const int32_t* a_m
 #define FP8_GEMM(KERNEL, GRID, THREADS) \
   KERNEL<<<GRID, THREADS, 0, s>>>(a, sa, (int)a_rows, a_map, a_div, offsets, E, (int)R_cap, w, sw, (int)N, (int)K, c)
   // Few rows per expert, and up to some 128 whatever their expert, leave tiles mostly empty
-  // or CUs idle (us here / in tiles, BF16 out: one expert of 5120 x 2048, 128 rows 19 / 23,
-  // 256 rows 26 / 23; 8 of 4096 x 2048, 192 rows 21 / 23, 256 rows 26 / 23; 128 of 1536 x 2048,
-  // 1024 rows 78 / 87, 2048 rows 100 / 91.  FP32 out, 128 of 2048 x 768: 1024 rows 47 / 52,
+  // or CUs idle (us here / in tiles, BF16 out: one expert of 5120 x 2048, 128 rows 18 / 25,
+  // 256 rows 27 / 26; 8 of 4096 x 2048, 192 rows 22 / 25, 256 rows 26 / 25; 128 of 1536 x 2048,
+  // 1024 rows 78 / 85, 2048 rows 99 / 89.  FP32 out, 128 of 2048 x 768: 1024 rows 46 / 52,
   // 2048 rows 58 / 54).
   if (R_cap <= 128 + 8 * (int64_t)E) {
     // sum of ceil(rows / 16) over the experts is at most this

@@ -13,13 +13,16 @@
 // the entry point):
 //   big    256 x 256 tiles, one persistent workgroup per CU, loads running into the
 //          next tile: 128 experts of 1536 x 2048 over 32768 rows, gathered, f32 out:
-//          509 us (1.61 GB of output at 3.2 TB/s, 405 TFLOP/s), bf16 out 381 us.  A fill
-//          of the output alone takes 237 us, the loads alone 289: the two add up,
-//          however they are interleaved;
+//          510 us (1.61 GB of output at 3.2 TB/s, 405 TFLOP/s), bf16 out 383 us.  The
+//          stores overlap with neither loads nor products: a fill of the output takes 237
+//          us, the loads alone 222, and it takes 457 with the products left out, 427 with
+//          the loads left out, 311 with the stores left out.  All eight wavefronts issue
+//          a tile's 32 stores together, on every CU at about the same time;
 //   mid    128 x 256 tiles, two workgroups per CU, one's stores beside the other's
 //          loads: the same 587 us, but less padding and finer balance;
 //   small  64 x 64 tiles, K split over the wavefronts: one expert of 4096 rows,
-//          1024 x 2048: 41 us (420 TFLOP/s; mid 142), latency of the K-steps.
+//          1024 x 2048: 38 us (450 TFLOP/s; mid 142): 32 K-steps to a wavefront, their
+//          loads requested one step ahead, so each pays most of a memory latency.
 #include "fp8.h"
 #include "lds_dma.h"
 
