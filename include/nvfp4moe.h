@@ -575,6 +575,104 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
                                          int32_t E, int64_t R_cap, int64_t M, int64_t N, void* c,
                                          int32_t c_dtype, void* stream);
 
+/*
+ * The router, the token sort and its way back, and their gradients: what lies between a
+ * router's logits and the experts' products.  Rows and logits are bf16 bits or float, by a
+ * type NVFP4_IN_BF16 or NVFP4_IN_F32; sums are taken in FP32 or FP64, and a bf16 result is
+ * rounded once, to nearest even.
+ *
+ * moe_router_topk - the k experts of each token and their weights.
+ *   logits   [T][E] of dtype
+ *   topk_ids out int32 [T][k]: the experts of the k largest logits, largest first; of equal
+ *            logits (0 and -0 are equal) the lower expert first; a NaN counts as the largest
+ *   topk_w   out float [T][k]: renorm 1: softmax over the k chosen logits (each token's
+ *            weights add up to 1); renorm 0: softmax over all E, the chosen experts' part
+ * An expert whose logit is -inf has the weight 0 and is chosen only if fewer than k others
+ * are left; a token whose logits are all -inf has k weights of 0.  A token that holds a NaN
+ * or a +inf has NaN weights.
+ *
+ * moe_router_topk_backward - dlogits [T][E] of dtype from the gradient of topk_w:
+ *     renorm 1: dlogits_e = sum over the token's entries s of expert e of w_s (g_s - m)
+ *     renorm 0: dlogits_e = p_e (sum over the entries s of e of g_s - m),  p = softmax(logits)
+ *   with g = dtopk_w and m = sum_s w_s g_s.  topk_ids and topk_w are moe_router_topk's; an
+ *   entry whose id is outside [0, E) is left out.  logits are read only with renorm 0 (NULL
+ *   otherwise).  Every element of dlogits is written.
+ * Both require 1 <= k <= min(E, NVFP4MOE_MAX_TOPK), E <= NVFP4MOE_MAX_EXPERTS,
+ * T * k <= INT32_MAX / 2.
+ *
+ * moe_permute - nvfp4_quantize_permute's routing for rows that are not quantised here:
+ * expert_offsets, row_to_tk and tk_to_row exactly as it writes them, and
+ *     rows[tk_to_row[t*k+s]] = x[t]   (copied bits)
+ *   x [T][H] of x_dtype; rows out [T*k][H]; both NULL: the maps alone (H and x_dtype unused)
+ *   workspace: nvfp4moe_permute_workspace_size(T, k, E) bytes, used as nvfp4_quantize_permute
+ *   uses it; dev_err as there
+ * rows and row_to_tk at or beyond expert_offsets[E] are left as they were.  Requires
+ * H % 8 == 0, 8 <= H <= MOE_MAX_H and the routing limits of nvfp4_quantize_permute.
+ * Its gradient is moe_combine without weights.
+ *
+ * moe_combine - y[t] = sum_s w_s d[tk_to_row[t*k+s]]: unpermute_combine for either type of
+ * rows and results, with the same sum (FP32, slot order, products and sums rounded apart;
+ * w_s = 1 when topk_w is NULL; entries outside [0, T*k) skipped).
+ *   d [T*k][H] of d_dtype; y out [T][H] of y_dtype
+ *
+ * moe_combine_backward - its gradient:
+ *     dd[tk_to_row[i]] = w_i dy[t]               (i = t*k+s; w_i = 1 when topk_w is NULL)
+ *     dtopk_w[i] = sum_h dy[t][h] d[tk_to_row[i]][h]   in FP32; 0 for an entry without a row
+ *   dy [T][H] of dy_dtype; d and dd [T*k][H] of d_dtype; dtopk_w float [T*k].  dd or
+ *   dtopk_w may be NULL (not computed), d too without dtopk_w.  Rows that no entry names
+ *   are left as they were.  tk_to_row names each row at most once.
+ * The three require H % 8 == 0, 8 <= H <= MOE_MAX_H, 1 <= k <= NVFP4MOE_MAX_TOPK,
+ * T * k <= INT32_MAX / 2.
+ *
+ * swiglu_backward_weights - swiglu_backward (the same dgu, bit for bit) with the gradient of
+ * the router weights that the SwiGLU applies:
+ *     dtopk_w[row_to_tk[r]] = sum_j dh[r][j] silu(g[r][j]) u[r][j]   in FP64, rounded once
+ *   tk_to_row int32 [R_cap], the inverse map: entries without a row have 0.  Arguments and
+ *   requirements otherwise as swiglu_backward with topk_w; R_cap <= INT32_MAX / 2.
+ *
+ * moe_grad_norm - norm = sqrt(sum of x^2 over the elements of n tensors), summed in FP64 in
+ * a fixed order and rounded once to float.
+ *   grads, dtypes, numel: HOST arrays of n device pointers, NVFP4_IN_* types and element
+ *   counts, read before the call returns.  A tensor may start at any element (no 16-byte
+ *   alignment) and may be empty.  norm out float [1] (device);
+ *   workspace: moe_grad_workspace_size(n) bytes, contents need not be initialised; calls
+ *   that share it must be ordered.
+ * moe_grad_clip - the norm, and out_j = grads_j * c with c = min(1, max_norm / (norm + 1e-6)),
+ * factor and products in FP64, rounded to float (and from there to bf16).  out: HOST array of n device
+ * pointers; out_j is grads_j itself (in place) or memory that overlaps no other tensor of
+ * the call (NVFP4_ERR_ARG).  A norm that is inf gives c = 0, a NaN one c = NaN.
+ * Requires max_norm >= 0 (inf: the norm alone, and a copy where not in place),
+ * n <= MOE_MAX_TENSORS, numel <= MOE_MAX_NUMEL.
+ */
+#define MOE_MAX_H (1 << 20)
+#define MOE_MAX_TENSORS 65536
+#define MOE_MAX_NUMEL (1ll << 38)
+NVFP4MOE_API int moe_router_topk(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k,
+                                 int32_t renorm, int32_t* topk_ids, float* topk_w, void* stream);
+NVFP4MOE_API int moe_router_topk_backward(const void* logits, int32_t dtype, const int32_t* topk_ids,
+                                          const float* topk_w, const float* dtopk_w, int64_t T, int32_t E,
+                                          int32_t k, int32_t renorm, void* dlogits, void* stream);
+NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t H, const int32_t* topk_ids,
+                             int32_t k, int32_t E, void* rows, int32_t* expert_offsets, int32_t* row_to_tk,
+                             int32_t* tk_to_row, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                             void* stream);
+NVFP4MOE_API int moe_combine(const void* d, int32_t d_dtype, int64_t T, int32_t k, int64_t H,
+                             const int32_t* tk_to_row, const float* topk_w, void* y, int32_t y_dtype,
+                             void* stream);
+NVFP4MOE_API int moe_combine_backward(const void* dy, int32_t dy_dtype, const void* d, int32_t d_dtype,
+                                      int64_t T, int32_t k, int64_t H, const int32_t* tk_to_row,
+                                      const float* topk_w, void* dd, float* dtopk_w, void* stream);
+NVFP4MOE_API int swiglu_backward_weights(const float* gu, const float* dh, int64_t R_cap, int64_t I,
+                                         const int32_t* expert_offsets, int32_t E, const float* topk_w,
+                                         const int32_t* row_to_tk, const int32_t* tk_to_row, uint16_t* dgu,
+                                         float* dtopk_w, void* stream);
+NVFP4MOE_API size_t moe_grad_workspace_size(int32_t n);
+NVFP4MOE_API int moe_grad_norm(const void* const* grads, const int32_t* dtypes, const int64_t* numel, int32_t n,
+                               float* norm, void* workspace, size_t workspace_bytes, void* stream);
+NVFP4MOE_API int moe_grad_clip(const void* const* grads, void* const* out, const int32_t* dtypes,
+                               const int64_t* numel, int32_t n, double max_norm, float* norm, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* Measurement aid (no part of the MoE computation): the device's practical
  * FP16 MFMA rate.  256 workgroups of 8 wavefronts (two per SIMD on a 256-CU
  * MI355X) each issue `iters` rounds of 8 independent v_mfma_f32_32x32x16_f16 on

@@ -34,6 +34,8 @@ Modules:
   combine   - un-permutation with top-k combine, and the gather for dgrad
   layer     - the chained MoE layer forward and BF16 dgrad backward
   wgrad     - the expert weight gradient in NVFP4, quantised along tokens
+  router    - the router's top-k choice, its weights and their gradient
+  gradients - gradients of the combine and of the SwiGLU's router weights, gradient norm and clipping
   fp8       - FP8 quantisation by blocks of 128, its grouped GEMM, the BF16 weight gradient
 """
-from . import formats, quantize, permute, gemm, swiglu, combine, layer, wgrad, fp8  # noqa: F401
+from . import formats, quantize, permute, gemm, swiglu, combine, layer, wgrad, fp8, router, gradients  # noqa: F401

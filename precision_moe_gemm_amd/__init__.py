@@ -91,6 +91,15 @@ SIGNATURES = {
                                 _c.c_int),
     "bf16_grouped_gemm_wgrad": ([_P, _I64, _I32, _P, _I64, _I32, _P, _P, _I32, _I64, _I64, _I64, _P, _I32, _P],
                                 _c.c_int),
+    "moe_router_topk": ([_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P], _c.c_int),
+    "moe_router_topk_backward": ([_P, _I32, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _P], _c.c_int),
+    "moe_permute": ([_P, _I32, _I64, _I64, _P, _I32, _I32, _P, _P, _P, _P, _P, _c.c_size_t, _P, _P], _c.c_int),
+    "moe_combine": ([_P, _I32, _I64, _I32, _I64, _P, _P, _P, _I32, _P], _c.c_int),
+    "moe_combine_backward": ([_P, _I32, _P, _I32, _I64, _I32, _I64, _P, _P, _P, _P, _P], _c.c_int),
+    "swiglu_backward_weights": ([_P, _P, _I64, _I64, _P, _I32, _P, _P, _P, _P, _P, _P], _c.c_int),
+    "moe_grad_workspace_size": ([_I32], _c.c_size_t),
+    "moe_grad_norm": ([_P, _P, _P, _I32, _P, _P, _c.c_size_t, _P], _c.c_int),
+    "moe_grad_clip": ([_P, _P, _P, _P, _I32, _c.c_double, _P, _P, _c.c_size_t, _P], _c.c_int),
     "nvfp4moe_mfma_ceiling": ([_I64, _P, _P], _c.c_int),
 }
 
@@ -776,6 +785,195 @@ def bf16_grouped_gemm_wgrad(g, x, expert_offsets, row_to_tk=None, k: int = 1, ga
     _call("bf16_grouped_gemm_wgrad", dev, g.data_ptr(), g_rows, g_k, x.data_ptr(), x_rows, x_k,
           _ptr(row_to_tk) if gather else None, expert_offsets.data_ptr(), E, R_cap, M, N, c.data_ptr(), code)
     return c
+
+
+# ---------------------------------------------------------------------- router, token sort, gradients
+def moe_router_topk(logits, k: int, renorm: bool = True, ids=None, weights=None):
+    """The k largest logits of each token (bf16 or f32 [T, E]; ties: the lower expert first) ->
+    (topk_ids i32 [T, k], topk_w f32 [T, k]): their softmax over the k, or over all E (renorm=False)."""
+    dev = _head(logits, "logits", _BF16_F32, 2)
+    T, E = logits.shape
+    ids = _give(ids, "ids", (T, k), torch.int32, _I32T, logits, dev)
+    weights = _give(weights, "weights", (T, k), torch.float32, _F32, logits, dev)
+    _call("moe_router_topk", dev, logits.data_ptr(), logits.dtype == torch.float32, T, E, k, bool(renorm),
+          ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def moe_router_topk_backward(dweights, ids, weights, logits, renorm: bool = True, dlogits=None):
+    """The gradient of moe_router_topk's logits [T, E] from that of its weights: dlogits [T, E] of the
+    logits' type.  ids and weights are moe_router_topk's [T, k]; with renorm the logits are not read."""
+    dev = _head(logits, "logits", _BF16_F32, 2)
+    _arg(ids, "ids", _I32T, dev, 2)
+    T, E = logits.shape
+    k = ids.shape[1]
+    if ids.shape[0] != T:
+        raise ValueError("ids must have one row per token")
+    _arg(weights, "weights", _F32, dev, numel=T * k)
+    _arg(dweights, "dweights", _F32, dev, numel=T * k)
+    dlogits = _give(dlogits, "dlogits", (T, E), logits.dtype, (logits.dtype,), logits, dev)
+    _call("moe_router_topk_backward", dev, logits.data_ptr(), logits.dtype == torch.float32, ids.data_ptr(),
+          weights.data_ptr(), dweights.data_ptr(), T, E, k, bool(renorm), dlogits.data_ptr())
+    return dlogits
+
+
+def moe_permute(x, topk_ids, E: int, workspace=None, dev_err=None, out=None):
+    """Route + permute without quantising.  x bf16 or f32 [T, H], or None for the maps alone.  Returns dict
+    with rows [T*k, H] (x's type; not with x None), expert_offsets [E+1], row_to_tk [T*k], tk_to_row [T*k]."""
+    dev = _head(topk_ids, "topk_ids", _I32T, 2)
+    T, k = topk_ids.shape
+    R, H = T * k, 0
+    shapes = {}
+    if x is not None:
+        _arg(x, "x", _BF16_F32, dev, 2)
+        if x.shape[0] != T:
+            raise ValueError("topk_ids must have one row per token")
+        H = x.shape[1]
+        shapes["rows"] = ((R, H), x.dtype, (x.dtype,))
+    shapes |= {"expert_offsets": ((E + 1,), torch.int32, _I32T), "row_to_tk": ((R,), torch.int32, _I32T),
+               "tk_to_row": ((R,), torch.int32, _I32T)}
+    o = out or {}
+    res = {n: _give(o.get(n), n, shp, dt, dts, topk_ids, dev) for n, (shp, dt, dts) in shapes.items()}
+    if workspace is None:
+        workspace = _empty((max(permute_workspace_size(T, k, E), 256),), torch.uint8, topk_ids)
+    _arg(workspace, "workspace", _U8, dev)
+    if dev_err is not None:
+        _arg(dev_err, "dev_err", _I32T, dev, numel=1)
+    _call("moe_permute", dev, _ptr(x), x is not None and x.dtype == torch.float32, T, H, topk_ids.data_ptr(), k, E,
+          _ptr(res.get("rows")), res["expert_offsets"].data_ptr(), res["row_to_tk"].data_ptr(),
+          res["tk_to_row"].data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(dev_err))
+    return res
+
+
+def _entries(tk_to_row, k, dev):
+    """Tokens of a map of T * k entries."""
+    _arg(tk_to_row, "tk_to_row", _I32T, dev)
+    if k < 1 or tk_to_row.numel() % k:
+        raise ValueError("tk_to_row must hold T * k entries")
+    return tk_to_row.numel() // k
+
+
+def moe_combine(d, tk_to_row, k: int, topk_w=None, y=None, out_dtype=None):
+    """y[t] = sum over slots of w * d[row(t, slot)]; d bf16 or f32 [T*k, H].  Returns y [T, H], bfloat16
+    (default) or float32 (out_dtype=torch.float32, or an f32 `y`).  Without weights: moe_permute's gradient."""
+    dev = _head(d, "d", _BF16_F32, 2)
+    T = _entries(tk_to_row, k, dev)
+    H = d.shape[1]
+    _arg(d, "d", _BF16_F32, dev, numel=T * k * H)
+    if topk_w is not None:
+        _arg(topk_w, "topk_w", _F32, dev, numel=T * k)
+    if out_dtype is None and y is None:
+        out_dtype = torch.bfloat16
+    dt, dtypes, code = _out_dtype(y, out_dtype)
+    y = _give(y, "y", (T, H), dt, dtypes, d, dev)
+    _call("moe_combine", dev, d.data_ptr(), d.dtype == torch.float32, T, k, H, tk_to_row.data_ptr(), _ptr(topk_w),
+          y.data_ptr(), code == OUT_F32)
+    return y
+
+
+def moe_combine_backward(dy, d, tk_to_row, k: int, topk_w=None, dd=None, dw=None, want_dd: bool = True):
+    """The gradient of moe_combine: (dd [T*k, H], dw f32 [T, k]) from dy [T, H], both bf16 or f32.  dd has
+    d's type; with d None only dd is computed, of dy's type (or the given dd's); want_dd=False: only dw."""
+    dev = _head(dy, "dy", _BF16_F32, 2)
+    T, H = dy.shape
+    if _entries(tk_to_row, k, dev) != T:
+        raise ValueError("tk_to_row must hold T * k entries for dy [T, H]")
+    if d is not None:
+        _arg(d, "d", _BF16_F32, dev, 2, numel=T * k * H)
+        if d.shape[1] != H:
+            raise ValueError("d and dy must have the same row length")
+        dw = _give(dw, "dw", (T, k), torch.float32, _F32, dy, dev)
+        dt = d.dtype
+    else:
+        if dw is not None or not want_dd:
+            raise ValueError("dw needs d")
+        dt = dy.dtype if dd is None else dd.dtype
+    if topk_w is not None:
+        _arg(topk_w, "topk_w", _F32, dev, numel=T * k)
+    dd = _give(dd, "dd", (T * k, H), dt, _F32 if dt == torch.float32 else _BF16, dy, dev) if want_dd else None
+    _call("moe_combine_backward", dev, dy.data_ptr(), dy.dtype == torch.float32, _ptr(d), dt == torch.float32, T, k, H,
+          tk_to_row.data_ptr(), _ptr(topk_w), _ptr(dd), _ptr(dw))
+    return dd, dw
+
+
+def swiglu_backward_weights(gu, dh, expert_offsets, topk_w, row_to_tk, tk_to_row, dgu=None, dw=None):
+    """swiglu_backward with the gradient of the router weights too: (dgu bf16 [R_cap, 2I], dw f32 of
+    topk_w's shape; entries without a row have 0)."""
+    dev = _head(gu, "gu", _F32, 2)
+    _arg(expert_offsets, "expert_offsets", _I32T, dev)
+    R_cap, I2 = gu.shape
+    if I2 % 2:
+        raise ValueError("gu must have 2 I columns")
+    _arg(dh, "dh", _F32, dev, 2, numel=R_cap * (I2 // 2))
+    _arg(topk_w, "topk_w", _F32, dev)
+    if topk_w.numel() != R_cap:
+        raise ValueError(f"topk_w holds {topk_w.numel()} weights for {R_cap} rows")
+    _arg(row_to_tk, "row_to_tk", _I32T, dev, numel=R_cap)
+    _arg(tk_to_row, "tk_to_row", _I32T, dev, numel=R_cap)
+    dgu = _give(dgu, "dgu", (R_cap, I2), torch.bfloat16, _BF16, gu, dev)
+    dw = _give(dw, "dw", tuple(topk_w.shape), torch.float32, _F32, gu, dev)
+    _call("swiglu_backward_weights", dev, gu.data_ptr(), dh.data_ptr(), R_cap, I2 // 2, expert_offsets.data_ptr(),
+          expert_offsets.numel() - 1, topk_w.data_ptr(), row_to_tk.data_ptr(), tk_to_row.data_ptr(), dgu.data_ptr(),
+          dw.data_ptr())
+    return dgu, dw
+
+
+def grad_workspace_size(n: int) -> int:
+    """Device workspace bytes of grad_norm and grad_clip for n tensors."""
+    return int(load_library().moe_grad_workspace_size(n))
+
+
+def _grads(grads, what, dev):
+    """The tensors' (pointers, types, sizes) as C arrays, and their device."""
+    for j, t in enumerate(grads):
+        if dev is None:
+            dev = _head(t, f"{what}[0]", _BF16_F32, None)
+        _arg(t, f"{what}[{j}]", _BF16_F32, dev)
+    n = len(grads)
+    return ((_P * n)(*[t.data_ptr() for t in grads]), (_I32 * n)(*[t.dtype == torch.float32 for t in grads]),
+            (_I64 * n)(*[t.numel() for t in grads]), dev)
+
+
+def _grad_buffers(n, norm, workspace, dev):
+    where = torch.device("cuda", dev)
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=where)
+    else:
+        _arg(norm, "norm", _F32, dev, numel=1)
+    if workspace is None:
+        workspace = torch.empty(max(grad_workspace_size(n), 256), dtype=torch.uint8, device=where)
+    else:
+        _arg(workspace, "workspace", _U8, dev)
+    return norm, workspace
+
+
+def grad_norm(grads, norm=None, workspace=None):
+    """sqrt of the sum of squares over all elements of the tensors (bf16 or f32, any shapes and alignment):
+    a float32 device tensor [1]."""
+    grads = list(grads)
+    ptrs, types, sizes, dev = _grads(grads, "grads", None if norm is None else norm.get_device())
+    dev = torch.cuda.current_device() if dev is None else dev
+    norm, workspace = _grad_buffers(len(grads), norm, workspace, dev)
+    _call("moe_grad_norm", dev, ptrs, types, sizes, len(grads), norm.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return norm
+
+
+def grad_clip(grads, max_norm: float, out=None, norm=None, workspace=None):
+    """Scale the tensors by min(1, max_norm / (norm + 1e-6)), norm as grad_norm's: (norm f32 [1], out).
+    `out`: tensors of the same sizes and types; `out=grads` clips in place; None: new ones."""
+    grads = list(grads)
+    ptrs, types, sizes, dev = _grads(grads, "grads", None if norm is None else norm.get_device())
+    dev = torch.cuda.current_device() if dev is None else dev
+    out = [torch.empty_like(t) for t in grads] if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError(f"{len(out)} outputs for {len(grads)} tensors")
+    outs, otypes, osizes, _ = _grads(out, "out", dev)
+    if list(otypes) != list(types) or list(osizes) != list(sizes):
+        raise ValueError("out must have the sizes and types of grads")
+    norm, workspace = _grad_buffers(len(grads), norm, workspace, dev)
+    _call("moe_grad_clip", dev, ptrs, outs, types, sizes, len(grads), max_norm, norm.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
+    return norm, out
 
 
 def mfma_ceiling(iters: int, sink=None):

@@ -7,6 +7,7 @@
 // §Two complementary interventions: device-side metadata, independent
 // forward/backward precision).
 #include "common.h"
+#include "rows.h"
 
 namespace nvfp4moe {
 
@@ -136,20 +137,30 @@ __global__ __launch_bounds__(256) void permute_gather_kernel(
 }
 
 // Gradient of h = w * silu(g) * u in float64 (sigmoid_f64, within 2^-50 of the
-// sigmoid; silu = g * sigmoid), each output rounded once to bf16.
+// sigmoid; silu = g * sigmoid), each output rounded once to bf16.  DW: also w's, the sum over the row of
+// dh * silu(g) * u in float64, rounded once to float32.  The wavefront of row r then also looks at entry r
+// and writes 0 for one that has no row, so that every entry of dw is written without a fill before.
+template <bool DW>
 __global__ __launch_bounds__(256) void swiglu_backward_kernel(
     const float* __restrict__ gu, const float* __restrict__ dh, int64_t R_cap, int I,
     const int32_t* __restrict__ offsets, int E, const float* __restrict__ topk_w,
-    const int32_t* __restrict__ row_to_tk, uint16_t* __restrict__ dgu) {
+    const int32_t* __restrict__ row_to_tk, uint16_t* __restrict__ dgu, const int32_t* __restrict__ tk_to_row,
+    float* __restrict__ dw) {
   __shared__ double exp2_tab[64];
   stage_exp2_table(exp2_tab);
   const int64_t r = (int64_t)blockIdx.x * kRows + (threadIdx.x >> 6);
+  if (DW && r < R_cap && lane_id() == 0) {
+    const int32_t at = tk_to_row[r];
+    if (at < 0 || at >= R_cap || at >= offsets[E]) dw[r] = 0.0f;
+  }
   if (r >= offsets[E] || r >= R_cap) return;
   float w = 1.0f;
+  int32_t entry = -1;
   if (topk_w) {   // the router weight of the row's (token, slot); a bad map entry gives 0
-    const int32_t i = row_to_tk[r];
-    w = (i >= 0 && i < R_cap) ? topk_w[i] : 0.0f;
+    entry = row_to_tk[r];
+    w = (entry >= 0 && entry < R_cap) ? topk_w[entry] : 0.0f;
   }
+  double sum = 0.0;
   const float* grow = gu + r * (int64_t)(2 * I);
   const float* drow = dh + r * (int64_t)I;
   uint16_t* orow = dgu + r * (int64_t)(2 * I);
@@ -172,6 +183,7 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(
         const double sig = sigmoid_f64(gs[j + q], exp2_tab);
         const double silu = g * sig;
         const double du = t * silu;
+        if (DW) sum = __builtin_fma((double)ds[j + q] * silu, u, sum);
         const double dg = (t * u) * (sig * (1.0 + g * (1.0 - sig)));
         bg[q] = f64_to_bf16_rne(dg);
         bu[q] = f64_to_bf16_rne(du);
@@ -181,6 +193,10 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(
     }
     *reinterpret_cast<uint2*>(orow + base) = make_uint2(og[0], og[1]);
     *reinterpret_cast<uint2*>(orow + I + base) = make_uint2(ou[0], ou[1]);
+  }
+  if (DW) {
+    sum = wave_sum(sum);
+    if (lane_id() == 0 && entry >= 0 && entry < R_cap) dw[entry] = (float)sum;
   }
 }
 
@@ -267,8 +283,24 @@ NVFP4MOE_API int swiglu_backward(const float* gu, const float* dh, int64_t R_cap
   if (topk_w && !row_to_tk) return NVFP4_ERR_NULL;
   if (!aligned16(gu) || !aligned16(dh) || !aligned16(dgu)) return NVFP4_ERR_ALIGN;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  swiglu_backward_kernel<<<(unsigned)((R_cap + kRows - 1) / kRows), 256, 0, s>>>(
-      gu, dh, R_cap, (int)I, expert_offsets, E, topk_w, row_to_tk, dgu);
+  swiglu_backward_kernel<false><<<(unsigned)((R_cap + kRows - 1) / kRows), 256, 0, s>>>(
+      gu, dh, R_cap, (int)I, expert_offsets, E, topk_w, row_to_tk, dgu, nullptr, nullptr);
+  return launch_status();
+}
+
+NVFP4MOE_API int swiglu_backward_weights(const float* gu, const float* dh, int64_t R_cap, int64_t I,
+                                         const int32_t* expert_offsets, int32_t E, const float* topk_w,
+                                         const int32_t* row_to_tk, const int32_t* tk_to_row, uint16_t* dgu,
+                                         float* dtopk_w, void* stream) {
+  if (R_cap < 0 || R_cap > INT32_MAX / 2 || I <= 0 || I % 8 != 0 || I > INT32_MAX / 4) return NVFP4_ERR_SHAPE;
+  if (E < 1 || E > NVFP4MOE_MAX_EXPERTS) return NVFP4_ERR_SHAPE;
+  if (R_cap == 0) return NVFP4_OK;
+  if (!gu || !dh || !expert_offsets || !topk_w || !row_to_tk || !tk_to_row || !dgu || !dtopk_w) return NVFP4_ERR_NULL;
+  if (!aligned16(gu) || !aligned16(dh) || !aligned16(dgu)) return NVFP4_ERR_ALIGN;
+  if (dtopk_w == topk_w) return NVFP4_ERR_ARG;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  swiglu_backward_kernel<true><<<(unsigned)((R_cap + kRows - 1) / kRows), 256, 0, s>>>(
+      gu, dh, R_cap, (int)I, expert_offsets, E, topk_w, row_to_tk, dgu, tk_to_row, dtopk_w);
   return launch_status();
 }
 

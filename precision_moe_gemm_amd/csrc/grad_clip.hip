@@ -1,0 +1,310 @@
+// The norm of the gradients over many tensors, and clipping by it, for gfx950.  Both stream the tensors
+// once; clipping streams them a second time, in and out.  Bound by memory.
+//
+// The tensors' addresses go to the kernels by value, kTensors a launch, so that no table has to be copied
+// to the device first.  A launch's work is cut into pieces of kPiece bytes; workgroup b takes pieces b,
+// b + grid, ... and leaves one partial sum of squares.  Squares of bf16 and float32 values are exact in
+// float64, and their float64 sums, in an order that depends on the sizes and the alignment alone, are off
+// by far less than a float32 step, so the norm is rounded once.
+#include <algorithm>
+#include <new>
+
+#include "common.h"
+#include "rows.h"
+
+namespace nvfp4moe {
+namespace gc {
+
+constexpr int kTensors = 96;          // tensors a launch (the kernel arguments hold 4 KB)
+constexpr int kThreads = 256;
+constexpr int kPiece = 65536;         // bytes of a piece, 16-byte words of one tensor
+constexpr int kPieceWords = kPiece / 16;
+constexpr int kPartials = 1024;       // workgroups over all launches (more where launches are more)
+
+struct Table {
+  const void* in[kTensors];
+  void* out[kTensors];
+  int64_t numel[kTensors];
+  int32_t first[kTensors + 1];        // the first piece of each tensor
+  uint8_t f32[kTensors];
+  int32_t n;
+};
+
+// Elements before the first 16-byte boundary of p.
+__host__ __device__ inline int64_t head_of(const void* p, int64_t numel, int size) {
+  const int64_t h = (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / size;
+  return h < numel ? h : numel;
+}
+
+// A piece: the 16-byte words [w0, w1) of a tensor behind its head; the first piece also has the head and
+// the tail, elements that fill no word.
+struct Piece {
+  int j;
+  int64_t head, words, w0, w1;
+  bool first;
+};
+
+__device__ __forceinline__ Piece piece_of(const Table& t, int p) {
+  int lo = 0, hi = t.n;               // the last tensor whose first piece is at or before p
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.first[mid] <= p) lo = mid; else hi = mid;
+  }
+  Piece q;
+  q.j = lo;
+  const int size = t.f32[lo] ? 4 : 2;
+  q.head = head_of(t.in[lo], t.numel[lo], size);
+  q.words = (t.numel[lo] - q.head) * size / 16;
+  q.w0 = (int64_t)(p - t.first[lo]) * kPieceWords;
+  q.w1 = min(q.words, q.w0 + kPieceWords);
+  q.first = p == t.first[lo];
+  return q;
+}
+
+template <bool F32>
+__device__ __forceinline__ double squares(uint4 v, double acc) {
+  if constexpr (F32) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) { const double d = __uint_as_float(w[j]); acc = __builtin_fma(d, d, acc); }
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const double a = bf16_lo(w[j]), b = bf16_hi(w[j]);
+      acc = __builtin_fma(a, a, acc);
+      acc = __builtin_fma(b, b, acc);
+    }
+  }
+  return acc;
+}
+
+template <bool F32>
+__device__ __forceinline__ double piece_squares(const void* p, int64_t numel, const Piece& q) {
+  constexpr int V = F32 ? 4 : 8;
+  const uint4* words = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + q.head * (F32 ? 4 : 2));
+  double acc = 0.0;
+  for (int64_t w = q.w0 + threadIdx.x; w < q.w1; w += kThreads) acc = squares<F32>(words[w], acc);
+  if (q.first) {
+    const int64_t tail = q.head + q.words * V, rest = q.head + numel - tail;   // head and tail elements
+    for (int64_t i = threadIdx.x; i < rest; i += kThreads) {
+      const double d = load_one<F32>(p, i < q.head ? i : tail + (i - q.head));
+      acc = __builtin_fma(d, d, acc);
+    }
+  }
+  return acc;
+}
+
+// the workgroup's sum in thread 0
+__device__ __forceinline__ double block_sum(double v, double* lds) {
+  v = wave_sum(v);
+  if (lane_id() == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = 0.0;
+  if (threadIdx.x == 0)
+    for (unsigned w = 0; w < blockDim.x / kWave; ++w) s += lds[w];
+  return s;
+}
+
+__global__ __launch_bounds__(kThreads) void squares_kernel(const Table t, double* __restrict__ partial) {
+  __shared__ double lds[kThreads / kWave];
+  double acc = 0.0;
+  for (int p = blockIdx.x; p < t.first[t.n]; p += gridDim.x) {
+    const Piece q = piece_of(t, p);
+    acc += t.f32[q.j] ? piece_squares<true>(t.in[q.j], t.numel[q.j], q) : piece_squares<false>(t.in[q.j], t.numel[q.j], q);
+  }
+  acc = block_sum(acc, lds);
+  if (threadIdx.x == 0) partial[blockIdx.x] = acc;
+}
+
+// The norm from n partial sums, in every thread, in an order that is the same in every workgroup.
+__device__ __forceinline__ double norm_of(const double* __restrict__ partial, int n, double* lds) {
+  double acc = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) acc += partial[i];
+  acc = block_sum(acc, lds);
+  if (threadIdx.x == 0) lds[0] = __builtin_sqrt(acc);
+  __syncthreads();
+  return lds[0];
+}
+
+__global__ __launch_bounds__(kThreads) void norm_kernel(const double* __restrict__ partial, int n, float* __restrict__ norm) {
+  __shared__ double lds[kThreads / kWave];
+  const double v = norm_of(partial, n, lds);
+  if (threadIdx.x == 0) *norm = (float)v;
+}
+
+// x * c in float64, so that a factor below float32's normal range (a norm above 2^126) costs no bits
+__device__ __forceinline__ float times(float x, double c) { return (float)((double)x * c); }
+
+// out = in * c for one piece; words when in and out lie alike towards a 16-byte boundary
+template <bool F32>
+__device__ __forceinline__ void scale_piece(const void* in, void* out, int64_t numel, const Piece& q, double c) {
+  constexpr int V = F32 ? 4 : 8, size = F32 ? 4 : 2;
+  const int64_t tail = q.head + q.words * V;
+  if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(in) + q.head * size);
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<char*>(out) + q.head * size);
+    for (int64_t w = q.w0 + threadIdx.x; w < q.w1; w += kThreads) {
+      const uint4 v = src[w];
+      uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (F32) u[j] = __float_as_uint(times(__uint_as_float(u[j]), c));
+        else u[j] = bf16x2_rne(times(bf16_lo(u[j]), c), times(bf16_hi(u[j]), c));
+      }
+      dst[w] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  } else {
+    for (int64_t i = q.head + q.w0 * V + threadIdx.x; i < q.head + q.w1 * V; i += kThreads)
+      store_one<F32>(out, i, times(load_one<F32>(in, i), c));
+  }
+  if (q.first) {
+    const int64_t rest = q.head + numel - tail;
+    for (int64_t i = threadIdx.x; i < rest; i += kThreads) {
+      const int64_t at = i < q.head ? i : tail + (i - q.head);
+      store_one<F32>(out, at, times(load_one<F32>(in, at), c));
+    }
+  }
+}
+
+// c = min(1, max_norm / (norm + 1e-6)), NaN for a NaN norm.  A factor of 1 leaves tensors that are clipped
+// in place untouched.
+__global__ __launch_bounds__(kThreads) void scale_kernel(const Table t, const double* __restrict__ partial, int n,
+                                                         double max_norm, float* __restrict__ norm) {
+  __shared__ double lds[kThreads / kWave];
+  const double v = norm_of(partial, n, lds);
+  const double ratio = max_norm / (v + 1e-6);
+  const double c = ratio >= 1.0 ? 1.0 : ratio;
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
+  for (int p = blockIdx.x; p < t.first[t.n]; p += gridDim.x) {
+    const Piece q = piece_of(t, p);
+    if (c == 1.0 && t.in[q.j] == t.out[q.j]) continue;
+    if (t.f32[q.j]) scale_piece<true>(t.in[q.j], t.out[q.j], t.numel[q.j], q, c);
+    else scale_piece<false>(t.in[q.j], t.out[q.j], t.numel[q.j], q, c);
+  }
+}
+
+// ------------------------------------------------------------------ host
+inline int launches_of(int64_t n) { return (int)((n + kTensors - 1) / kTensors); }
+inline int blocks_each(int64_t n) { return std::max(1, kPartials / std::max(1, launches_of(n))); }
+
+int check(const void* const* in, const int32_t* dtype, const int64_t* numel, int32_t n) {
+  if (n < 0 || n > MOE_MAX_TENSORS) return NVFP4_ERR_SHAPE;
+  if (n && (!in || !dtype || !numel)) return NVFP4_ERR_NULL;
+  for (int i = 0; i < n; ++i) {
+    if (dtype[i] != NVFP4_IN_BF16 && dtype[i] != NVFP4_IN_F32) return NVFP4_ERR_ARG;
+    if (numel[i] < 0 || numel[i] > MOE_MAX_NUMEL) return NVFP4_ERR_SHAPE;
+    if (numel[i] && !in[i]) return NVFP4_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(in[i]) & (dtype[i] == NVFP4_IN_F32 ? 3 : 1)) return NVFP4_ERR_ALIGN;
+  }
+  return NVFP4_OK;
+}
+
+// Whether an output overlaps another output, or an input other than its own tensor's.
+int overlaps(const void* const* in, void* const* out, const int32_t* dtype, const int64_t* numel, int32_t n) {
+  struct Range { uintptr_t lo, hi; bool out; };
+  Range* r = new (std::nothrow) Range[2 * (size_t)n + 1];
+  if (!r) return NVFP4_ERR_SHAPE;
+  size_t m = 0;
+  for (int i = 0; i < n; ++i) {
+    const uintptr_t bytes = (uintptr_t)numel[i] * (dtype[i] == NVFP4_IN_F32 ? 4 : 2);
+    if (!bytes) continue;
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out[i]), a = reinterpret_cast<uintptr_t>(in[i]);
+    r[m++] = {o, o + bytes, true};
+    if (o != a) r[m++] = {a, a + bytes, false};
+  }
+  std::sort(r, r + m, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t any = 0, outs = 0;
+  int bad = NVFP4_OK;
+  for (size_t i = 0; i < m; ++i) {
+    if (r[i].lo < (r[i].out ? any : outs)) bad = NVFP4_ERR_ARG;
+    any = std::max(any, r[i].hi);
+    if (r[i].out) outs = std::max(outs, r[i].hi);
+  }
+  delete[] r;
+  return bad;
+}
+
+// Tensors [i0, n) into a table until it is full; returns the first that is not in it.  Empty tensors are
+// left out.  (kTensors tensors of MOE_MAX_NUMEL elements have fewer than 2^31 - 2^11 pieces.)
+int fill(Table& t, const void* const* in, void* const* out, const int32_t* dtype, const int64_t* numel, int i0, int n) {
+  t.n = 0;
+  t.first[0] = 0;
+  int i = i0;
+  for (; i < n && t.n < kTensors; ++i) {
+    if (!numel[i]) continue;
+    const int j = t.n, size = dtype[i] == NVFP4_IN_F32 ? 4 : 2;
+    const int64_t words = (numel[i] - head_of(in[i], numel[i], size)) * size / 16;
+    const int64_t pieces = std::max<int64_t>(1, (words + kPieceWords - 1) / kPieceWords);
+    t.in[j] = in[i];
+    t.out[j] = out ? out[i] : nullptr;
+    t.numel[j] = numel[i];
+    t.f32[j] = dtype[i] == NVFP4_IN_F32;
+    t.first[j + 1] = t.first[j] + (int)pieces;
+    t.n = j + 1;
+  }
+  return i;
+}
+
+int run(const void* const* in, void* const* out, const int32_t* dtype, const int64_t* numel, int32_t n, double max_norm,
+        float* norm, double* partial, hipStream_t s) {
+  Table t;
+  const int most = blocks_each(n);
+  int used = 0;
+  for (int i = 0; i < n;) {
+    i = fill(t, in, out, dtype, numel, i, n);
+    if (!t.n) break;
+    const int grid = std::min(most, t.first[t.n]);
+    squares_kernel<<<grid, kThreads, 0, s>>>(t, partial + used);
+    used += grid;
+  }
+  if (!out || !used) {
+    norm_kernel<<<1, kThreads, 0, s>>>(partial, used, norm);
+    return launch_status();
+  }
+  for (int i = 0; i < n;) {
+    const bool first = i == 0;
+    i = fill(t, in, out, dtype, numel, i, n);
+    if (!t.n) break;
+    scale_kernel<<<std::min(2048, t.first[t.n]), kThreads, 0, s>>>(t, partial, used, max_norm, first ? norm : nullptr);
+  }
+  return launch_status();
+}
+
+}  // namespace gc
+}  // namespace nvfp4moe
+
+using namespace nvfp4moe;
+
+extern "C" {
+
+NVFP4MOE_API size_t moe_grad_workspace_size(int32_t n) {
+  if (n < 0 || n > MOE_MAX_TENSORS) return 0;
+  return (size_t)std::max(gc::kPartials, gc::launches_of(n)) * sizeof(double);
+}
+
+NVFP4MOE_API int moe_grad_norm(const void* const* grads, const int32_t* dtypes, const int64_t* numel, int32_t n,
+                               float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  if (const int bad = gc::check(grads, dtypes, numel, n)) return bad;
+  if (!norm || !workspace) return NVFP4_ERR_NULL;
+  if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(norm) & 3)) return NVFP4_ERR_ALIGN;
+  if (workspace_bytes < moe_grad_workspace_size(n)) return NVFP4_ERR_WORKSPACE;
+  return gc::run(grads, nullptr, dtypes, numel, n, 0.0, norm, static_cast<double*>(workspace),
+                 static_cast<hipStream_t>(stream));
+}
+
+NVFP4MOE_API int moe_grad_clip(const void* const* grads, void* const* out, const int32_t* dtypes, const int64_t* numel,
+                               int32_t n, double max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (!(max_norm >= 0.0)) return NVFP4_ERR_ARG;
+  if (const int bad = gc::check(grads, dtypes, numel, n)) return bad;
+  if (!norm || !workspace || (n && !out)) return NVFP4_ERR_NULL;
+  if (const int bad = gc::check(out, dtypes, numel, n)) return bad;
+  if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(norm) & 3)) return NVFP4_ERR_ALIGN;
+  if (workspace_bytes < moe_grad_workspace_size(n)) return NVFP4_ERR_WORKSPACE;
+  if (const int bad = gc::overlaps(grads, out, dtypes, numel, n)) return bad;
+  return gc::run(grads, out, dtypes, numel, n, max_norm, norm, static_cast<double*>(workspace),
+                 static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"
