@@ -604,8 +604,8 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  * expert_offsets, row_to_tk and tk_to_row exactly as it writes them, and
  *     rows[tk_to_row[t*k+s]] = x[t]   (copied bits)
  *   x [T][H] of x_dtype; rows out [T*k][H]; both NULL: the maps alone (H and x_dtype unused)
- *   workspace: nvfp4moe_permute_workspace_size(T, k, E) bytes, used as nvfp4_quantize_permute
- *   uses it; dev_err as there
+ *   workspace: moe_permute_workspace_size(T, k, E) bytes (0 for short routing lists: NULL),
+ *   used as nvfp4_quantize_permute uses its own; dev_err as there
  * rows and row_to_tk at or beyond expert_offsets[E] are left as they were.  Requires
  * H % 8 == 0, 8 <= H <= MOE_MAX_H and the routing limits of nvfp4_quantize_permute.
  * Its gradient is moe_combine without weights.
@@ -652,6 +652,7 @@ NVFP4MOE_API int moe_router_topk(const void* logits, int32_t dtype, int64_t T, i
 NVFP4MOE_API int moe_router_topk_backward(const void* logits, int32_t dtype, const int32_t* topk_ids,
                                           const float* topk_w, const float* dtopk_w, int64_t T, int32_t E,
                                           int32_t k, int32_t renorm, void* dlogits, void* stream);
+NVFP4MOE_API size_t moe_permute_workspace_size(int64_t T, int32_t k, int32_t E);
 NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t H, const int32_t* topk_ids,
                              int32_t k, int32_t E, void* rows, int32_t* expert_offsets, int32_t* row_to_tk,
                              int32_t* tk_to_row, void* workspace, size_t workspace_bytes, int32_t* dev_err,

@@ -93,6 +93,7 @@ SIGNATURES = {
                                 _c.c_int),
     "moe_router_topk": ([_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P], _c.c_int),
     "moe_router_topk_backward": ([_P, _I32, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _P], _c.c_int),
+    "moe_permute_workspace_size": ([_I64, _I32, _I32], _c.c_size_t),
     "moe_permute": ([_P, _I32, _I64, _I64, _P, _I32, _I32, _P, _P, _P, _P, _P, _c.c_size_t, _P, _P], _c.c_int),
     "moe_combine": ([_P, _I32, _I64, _I32, _I64, _P, _P, _P, _I32, _P], _c.c_int),
     "moe_combine_backward": ([_P, _I32, _P, _I32, _I64, _I32, _I64, _P, _P, _P, _P, _P], _c.c_int),
@@ -817,6 +818,11 @@ def moe_router_topk_backward(dweights, ids, weights, logits, renorm: bool = True
     return dlogits
 
 
+def moe_permute_workspace_size(T: int, k: int, E: int) -> int:
+    """Device workspace bytes of moe_permute: 0 for short routing lists."""
+    return int(load_library().moe_permute_workspace_size(T, k, E))
+
+
 def moe_permute(x, topk_ids, E: int, workspace=None, dev_err=None, out=None):
     """Route + permute without quantising.  x bf16 or f32 [T, H], or None for the maps alone.  Returns dict
     with rows [T*k, H] (x's type; not with x None), expert_offsets [E+1], row_to_tk [T*k], tk_to_row [T*k]."""
@@ -835,13 +841,15 @@ def moe_permute(x, topk_ids, E: int, workspace=None, dev_err=None, out=None):
     o = out or {}
     res = {n: _give(o.get(n), n, shp, dt, dts, topk_ids, dev) for n, (shp, dt, dts) in shapes.items()}
     if workspace is None:
-        workspace = _empty((max(permute_workspace_size(T, k, E), 256),), torch.uint8, topk_ids)
-    _arg(workspace, "workspace", _U8, dev)
+        need = load_library().moe_permute_workspace_size(T, k, E)
+        workspace = _empty((need,), torch.uint8, topk_ids) if need else None
+    else:
+        _arg(workspace, "workspace", _U8, dev)
     if dev_err is not None:
         _arg(dev_err, "dev_err", _I32T, dev, numel=1)
     _call("moe_permute", dev, _ptr(x), x is not None and x.dtype == torch.float32, T, H, topk_ids.data_ptr(), k, E,
           _ptr(res.get("rows")), res["expert_offsets"].data_ptr(), res["row_to_tk"].data_ptr(),
-          res["tk_to_row"].data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(dev_err))
+          res["tk_to_row"].data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(dev_err))
     return res
 
 
@@ -923,15 +931,26 @@ def grad_workspace_size(n: int) -> int:
     return int(load_library().moe_grad_workspace_size(n))
 
 
+_GRAD_TYPES = {torch.float32: 1, **dict.fromkeys(_BF16, 0)}
+
+
 def _grads(grads, what, dev):
     """The tensors' (pointers, types, sizes) as C arrays, and their device."""
+    n = len(grads)
+    # models hold hundreds of tensors, so the checks run over the whole list; the loop names the one that fails
+    if n and all(isinstance(t, torch.Tensor) for t in grads):
+        where = set(map(torch.Tensor.get_device, grads))
+        types = [_GRAD_TYPES.get(t.dtype, -1) for t in grads]
+        if len(where) == 1 and -1 not in types and all(map(torch.Tensor.is_contiguous, grads)):
+            at = where.pop()
+            if at >= 0 and dev in (None, at):
+                return ((_P * n)(*map(torch.Tensor.data_ptr, grads)), (_I32 * n)(*types),
+                        (_I64 * n)(*map(torch.Tensor.numel, grads)), at)
     for j, t in enumerate(grads):
         if dev is None:
             dev = _head(t, f"{what}[0]", _BF16_F32, None)
         _arg(t, f"{what}[{j}]", _BF16_F32, dev)
-    n = len(grads)
-    return ((_P * n)(*[t.data_ptr() for t in grads]), (_I32 * n)(*[t.dtype == torch.float32 for t in grads]),
-            (_I64 * n)(*[t.numel() for t in grads]), dev)
+    return (_P * 0)(), (_I32 * 0)(), (_I64 * 0)(), dev
 
 
 def _grad_buffers(n, norm, workspace, dev):
@@ -968,7 +987,7 @@ def grad_clip(grads, max_norm: float, out=None, norm=None, workspace=None):
     if len(out) != len(grads):
         raise ValueError(f"{len(out)} outputs for {len(grads)} tensors")
     outs, otypes, osizes, _ = _grads(out, "out", dev)
-    if list(otypes) != list(types) or list(osizes) != list(sizes):
+    if bytes(otypes) != bytes(types) or bytes(osizes) != bytes(sizes):
         raise ValueError("out must have the sizes and types of grads")
     norm, workspace = _grad_buffers(len(grads), norm, workspace, dev)
     _call("moe_grad_clip", dev, ptrs, outs, types, sizes, len(grads), max_norm, norm.data_ptr(), workspace.data_ptr(),

@@ -1,6 +1,8 @@
 // Token rows sorted by expert without quantising them, the weighted way back to token order, and its
 // gradient, for gfx950.  All are bound by memory: the sort reads every token row once and writes it k
 // times, the combine reads k rows for each that it writes, the gradient reads and writes k rows a token.
+#include <algorithm>
+
 #include "common.h"
 #include "route.h"
 #include "rows.h"
@@ -11,8 +13,80 @@ namespace mp {
 constexpr int kWaves = 4;       // wavefronts per 256-thread workgroup
 constexpr int kCols = 512;      // elements of a row that a wavefront takes at a time, 8 a lane
 
-// One wavefront per token: its entries' rows from the first rows of route_scan_kernel, the maps, and the
-// token's row (bytes, a multiple of 16) copied to them.
+// Rows go out with non-temporal stores: 4096 tokens x 8 rows of 4 KB take 27 us so and 36 with ordinary
+// ones (in both cases after other work has left the caches full of lines to write back).  The grouped
+// product that reads them next gains less from their being cached than that: permutation and a BF16 gate_up
+// product together take 169 us for 176 at 600 tokens, 202 for 201 at 2048, 247 for 249 at 4096, 361 for 381
+// at 8192.
+__device__ __forceinline__ void store_row(uint4* dst, uint4 v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(dst));
+}
+
+// A wavefront's part of a token's row: its first kHeld 16-byte words a lane stay in registers (rows up to
+// 4 KB), requested before the routing is known; longer rows are read again for what lies behind.
+constexpr int kHeld = 4;
+struct Row {
+  uint4 held[kHeld];
+  __device__ __forceinline__ void load(const uint4* __restrict__ src, int words) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) held[u] = src[min(u * kWave + lane_id(), words - 1)];
+  }
+  __device__ __forceinline__ void copy_held(uint4* __restrict__ dst, int words) const {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (u * kWave + lane_id() < words) store_row(dst + u * kWave + lane_id(), held[u]);
+  }
+};
+
+// The token's row to its k routed rows (row: lane s holds entry s's, -1 for none).
+__device__ __forceinline__ void copy_to_rows(const Row& held, const uint4* __restrict__ src, int words, int k, int row,
+                                             uint4* __restrict__ rows) {
+  for (int s = 0; s < k; ++s) {
+    const int r = __shfl(row, s, kWave);
+    if (r >= 0) held.copy_held(rows + (int64_t)r * words, words);
+  }
+  for (int c0 = kHeld * kWave; c0 < words; c0 += kWave) {
+    const int c = c0 + lane_id();
+    const uint4 v = src[min(c, words - 1)];
+    for (int s = 0; s < k; ++s) {
+      const int r = __shfl(row, s, kWave);
+      if (r >= 0 && c < words) store_row(rows + (int64_t)r * words + c, v);
+    }
+  }
+}
+
+// One wavefront per token, eight to a workgroup: the entries' rows from the count table and the ranks, the
+// maps, and the token's row copied to them.  The row is requested before the table is scanned.
+__global__ __launch_bounds__(kRouteThreads) void permute_kernel(
+    const uint4* __restrict__ x, int64_t T, int words, const int32_t* __restrict__ ids, int k, int E,
+    const int32_t* __restrict__ cnt, const int32_t* __restrict__ rank, int nchunks, int chunk_log,
+    uint4* __restrict__ rows, int32_t* __restrict__ offsets, int32_t* __restrict__ row_to_tk,
+    int32_t* __restrict__ tk_to_row) {
+  __shared__ RouteLds lds;
+  const int lane = lane_id();
+  const int64_t t = (int64_t)blockIdx.x * kRouteTokens + (threadIdx.x >> 6);
+  const int n = (int)(T * k);
+  RouteTable table;
+  table.c0 = (int)((int64_t)blockIdx.x * kRouteTokens * k) >> chunk_log;
+  table.load(cnt, nchunks * E);
+  const int i = (int)(t * k) + lane;
+  const int e = ids[min(i, n - 1)], r = rank[min(i, n - 1)];
+  const uint4* src = x + min(t, T - 1) * words;
+  Row held;
+  if (rows) held.load(src, words);
+  table.scan(lds, nchunks, E, offsets);
+  if (t >= T) return;
+  int row = -1;
+  if (lane < k) {
+    if (r >= 0) row = lds.first[(i >> chunk_log) - table.c0][e] + r;   // a rank marks a valid expert id
+    tk_to_row[i] = row;
+    if (row >= 0) row_to_tk[row] = i;
+  }
+  if (rows) copy_to_rows(held, src, words, k, row, rows);
+}
+
+// The same from the first rows of route_scan_kernel: long routing lists.
 __global__ __launch_bounds__(kWaves * 64) void permute_rows_kernel(
     const uint4* __restrict__ x, int64_t T, int words, const int32_t* __restrict__ ids, int k, int E,
     const int32_t* __restrict__ base, const int32_t* __restrict__ rank, int chunk_log, uint4* __restrict__ rows,
@@ -20,6 +94,9 @@ __global__ __launch_bounds__(kWaves * 64) void permute_rows_kernel(
   const int64_t t = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
   if (t >= T) return;
   const int lane = lane_id();
+  const uint4* src = x + t * words;
+  Row held;
+  if (rows) held.load(src, words);
   int row = -1;
   if (lane < k) {
     const int i = (int)(t * k) + lane;
@@ -28,14 +105,89 @@ __global__ __launch_bounds__(kWaves * 64) void permute_rows_kernel(
     tk_to_row[i] = row;
     if (row >= 0) row_to_tk[row] = i;
   }
+  if (rows) copy_to_rows(held, src, words, k, row, rows);
+}
+
+// Short routing lists in one launch: every workgroup reads the whole list, counts each expert's entries and
+// those before its own (LDS), scans the counts, and ranks the entries of its own `per` tokens; its
+// wavefronts then take one (token, slot) row each.
+constexpr int kShort = 6144;            // entries; 128 experts, in one launch and in two: 3072 entries 7.5 us
+                                        // for 9.8, 6144 10.0 for 10.8, 8192 12.2 for 12.2, 16384 21.9 for 19.2
+constexpr int kShortTokens = 8;         // most tokens a workgroup
+__global__ __launch_bounds__(kRouteThreads) void permute_short_kernel(
+    const uint4* __restrict__ x, int T, int words, const int32_t* __restrict__ ids, int k, int E, int per,
+    uint4* __restrict__ rows, int32_t* __restrict__ offsets, int32_t* __restrict__ row_to_tk,
+    int32_t* __restrict__ tk_to_row, int32_t* __restrict__ dev_err) {
+  __shared__ int32_t total[NVFP4MOE_MAX_EXPERTS], first[NVFP4MOE_MAX_EXPERTS];
+  __shared__ int32_t own_e[kShortTokens * NVFP4MOE_MAX_TOPK], own_row[kShortTokens * NVFP4MOE_MAX_TOPK];
+  __shared__ int32_t wsum[kRouteWaves];
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
+  const int n = T * k, t0 = blockIdx.x * per, e0 = t0 * k, own = min(per, T - t0) * k;
+  for (int e = tid; e < E; e += kRouteThreads) total[e] = first[e] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int i = tid; i < n; i += kRouteThreads) {
+    const int e = ids[i];
+    const bool valid = e >= 0 && e < E;
+    if (valid) {
+      atomicAdd(&total[e], 1);
+      if (i < e0) atomicAdd(&first[e], 1);
+    }
+    bad |= !valid;
+    if (i >= e0 && i < e0 + own) own_e[i - e0] = valid ? e : -1;
+  }
+  if (bad && dev_err && blockIdx.x == 0) atomicOr(dev_err, NVFP4_DEVERR_BAD_EXPERT);
+  __syncthreads();
+  int tot[kRouteExp], sum = 0;
+#pragma unroll
+  for (int u = 0; u < kRouteExp; ++u) {
+    const int e = kRouteExp * tid + u;
+    tot[u] = e < E ? total[e] : 0;
+    sum += tot[u];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int y = __shfl_up(incl, off, kWave);
+    if (lane >= off) incl += y;
+  }
+  if (lane == kWave - 1) wsum[wave] = incl;
+  __syncthreads();
+  int at = incl - sum;
+  for (int w = 0; w < wave; ++w) at += wsum[w];
+#pragma unroll
+  for (int u = 0; u < kRouteExp; ++u) {
+    const int e = kRouteExp * tid + u;
+    if (e < E) {
+      first[e] += at;
+      if (blockIdx.x == 0) offsets[e] = at;
+    }
+    at += tot[u];
+  }
+  if (blockIdx.x == 0 && tid == kRouteThreads - 1) offsets[E] = at;
+  __syncthreads();
+  if (tid < own) {
+    const int e = own_e[tid];
+    int row = -1;
+    if (e >= 0) {
+      row = first[e];
+      for (int j = 0; j < tid; ++j) row += own_e[j] == e;
+      row_to_tk[row] = e0 + tid;
+    }
+    tk_to_row[e0 + tid] = row;
+    own_row[tid] = row;
+  }
   if (!rows) return;
-  for (int c0 = 0; c0 < words; c0 += kWave) {
-    const int c = c0 + lane;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (c < words) v = x[t * words + c];
-    for (int s = 0; s < k; ++s) {
-      const int r = __shfl(row, s, kWave);
-      if (r >= 0 && c < words) rows[(int64_t)r * words + c] = v;
+  __syncthreads();
+  for (int q = wave; q < own; q += kRouteWaves) {
+    const int row = own_row[q];
+    if (row < 0) continue;
+    const uint4* src = x + (int64_t)(t0 + q / k) * words;
+    uint4* dst = rows + (int64_t)row * words;
+    for (int c0 = 0; c0 < words; c0 += kHeld * kWave) {
+      Row r;
+      r.load(src + c0, words - c0);
+      r.copy_held(dst + c0, words - c0);
     }
   }
 }
@@ -85,7 +237,10 @@ __global__ __launch_bounds__(kWaves * 64) void combine_kernel(
 }
 
 // One wavefront per entry i = (t, s): dd[row] = w_i dy[t], dw_i = <dy[t], d[row]> in FP32, added within
-// the lane and then over the wavefront in a fixed order.  An entry without a row has dw_i = 0.
+// the lane and then over the wavefront in a fixed order.  An entry without a row has dw_i = 0.  The loads of
+// kAhead pieces of 512 columns are issued before the first is used (4096 tokens x 8 rows of 2048 bf16: 58 us
+// with 4, 65 with 2, 70 with 1; 285 MB, so 4.9 TB/s); the token's k wavefronts share dy[t] in the caches.
+constexpr int kAhead = 4;
 template <bool YF32, bool DF32>
 __global__ __launch_bounds__(kWaves * 64) void combine_backward_kernel(
     const void* __restrict__ dy, const void* __restrict__ d, int64_t R, int k, int H,
@@ -100,18 +255,31 @@ __global__ __launch_bounds__(kWaves * 64) void combine_backward_kernel(
   float sum = 0.0f;
   if (has) {
     const float w = topk_w ? topk_w[i] : 1.0f;
-    for (int c = 8 * lane; c < H; c += kCols) {
-      float g[8], v[8];
-      unpack8<YF32>(load8<YF32>(dy, t * H + c), g);
-      if (dw) {
-        unpack8<DF32>(load8<DF32>(d, row * H + c), v);
+    for (int c0 = 8 * lane; c0 < H; c0 += kAhead * kCols) {
+      Raw8<YF32> yr[kAhead];
+      Raw8<DF32> dr[kAhead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(g[j], v[j], sum);
+      for (int u = 0; u < kAhead; ++u) {
+        const int c = min(c0 + u * kCols, H - 8);
+        yr[u] = load8<YF32>(dy, t * H + c);
+        if (dw) dr[u] = load8<DF32>(d, row * H + c);
       }
-      if (dd) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = w * g[j];
-        store8<DF32>(dd, row * H + c, v);
+      for (int u = 0; u < kAhead; ++u) {
+        const int c = c0 + u * kCols;
+        if (c >= H) continue;
+        float y[8], v[8];
+        unpack8<YF32>(yr[u], y);
+        if (dw) {
+          unpack8<DF32>(dr[u], v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(y[j], v[j], sum);
+        }
+        if (dd) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = w * y[j];
+          store8<DF32>(dd, row * H + c, v);
+        }
       }
     }
   }
@@ -135,32 +303,48 @@ using namespace nvfp4moe;
 
 extern "C" {
 
+NVFP4MOE_API size_t moe_permute_workspace_size(int64_t T, int32_t k, int32_t E) {
+  return T > 0 && T * (int64_t)k <= mp::kShort ? 0 : nvfp4moe_permute_workspace_size(T, k, E);
+}
+
 NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t H, const int32_t* topk_ids, int32_t k,
                              int32_t E, void* rows, int32_t* expert_offsets, int32_t* row_to_tk, int32_t* tk_to_row,
                              void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream) {
   if (!mp::type_ok(x_dtype)) return NVFP4_ERR_ARG;
   if (const int bad = mp::check(T, k, x || rows ? H : 8)) return bad;
   if (E < 1 || E > NVFP4MOE_MAX_EXPERTS || k > E) return NVFP4_ERR_SHAPE;
-  if (!expert_offsets || !workspace) return NVFP4_ERR_NULL;
+  const size_t need = moe_permute_workspace_size(T, k, E);
+  if (!expert_offsets || (need && !workspace)) return NVFP4_ERR_NULL;
   if (T > 0 && (!topk_ids || !row_to_tk || !tk_to_row || !x != !rows)) return NVFP4_ERR_NULL;
   if (!aligned16(x) || !aligned16(topk_ids) || !aligned16(rows) || !aligned16(expert_offsets) ||
       !aligned16(row_to_tk) || !aligned16(tk_to_row) || !aligned16(workspace))
     return NVFP4_ERR_ALIGN;
   if (x && x == rows) return NVFP4_ERR_ARG;
-  if (workspace_bytes < nvfp4moe_permute_workspace_size(T, k, E)) return NVFP4_ERR_WORKSPACE;
+  if (workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t n = T * (int64_t)k;
+  const int words = (int)(H * (x_dtype == NVFP4_IN_F32 ? 4 : 2) / 16);
+  const uint4* src = static_cast<const uint4*>(x);
+  uint4* dst = static_cast<uint4*>(rows);
+  if (T > 0 && n <= mp::kShort) {
+    const int per = (int)std::min<int64_t>(mp::kShortTokens, (T + 255) / 256);
+    mp::permute_short_kernel<<<(unsigned)((T + per - 1) / per), kRouteThreads, 0, s>>>(
+        src, (int)T, words, topk_ids, k, E, per, dst, expert_offsets, row_to_tk, tk_to_row, dev_err);
+    return launch_status();
+  }
   const int chunk_log = plan_chunk_log(n, E), chunks = plan_chunks(n, chunk_log);
   int32_t* table = static_cast<int32_t*>(workspace);        // [chunks][E]
   int32_t* rank = table + (int64_t)chunks * E;              // [n]
   route_rank_kernel<<<chunks, kPlanThreads, 0, s>>>(topk_ids, (int)n, E, chunk_log, table, rank, dev_err);
-  route_scan_kernel<<<1, kPlanThreads, 0, s>>>(table, chunks, E, expert_offsets);
-  if (T > 0) {
-    const int words = (int)(H * (x_dtype == NVFP4_IN_F32 ? 4 : 2) / 16);
-    mp::permute_rows_kernel<<<(unsigned)((T + mp::kWaves - 1) / mp::kWaves), mp::kWaves * 64, 0, s>>>(
-        static_cast<const uint4*>(x), T, words, topk_ids, k, E, table, rank, chunk_log, static_cast<uint4*>(rows),
-        row_to_tk, tk_to_row);
+  if (T > 0 && (int64_t)chunks * E <= kCountTable) {
+    mp::permute_kernel<<<(unsigned)((T + kRouteTokens - 1) / kRouteTokens), kRouteThreads, 0, s>>>(
+        src, T, words, topk_ids, k, E, table, rank, chunks, chunk_log, dst, expert_offsets, row_to_tk, tk_to_row);
+    return launch_status();
   }
+  route_scan_kernel<<<1, kPlanThreads, 0, s>>>(table, chunks, E, expert_offsets);
+  if (T > 0)
+    mp::permute_rows_kernel<<<(unsigned)((T + mp::kWaves - 1) / mp::kWaves), mp::kWaves * 64, 0, s>>>(
+        src, T, words, topk_ids, k, E, table, rank, chunk_log, dst, row_to_tk, tk_to_row);
   return launch_status();
 }
 

@@ -368,9 +368,8 @@ __global__ __launch_bounds__(256) void quantize_rows_tiled_kernel(
 // expert offsets.  Every load is issued unconditionally (indices clamped into
 // the arrays) and the workgroup barriers order LDS only, so that waiting for
 // the routing loads leaves the activations in flight.
-constexpr int kQpWaves = 8;
-constexpr int kQpThreads = kQpWaves * 64;
-constexpr int kQpExp = NVFP4MOE_MAX_EXPERTS / kQpThreads;   // experts per thread (2)
+constexpr int kQpWaves = kRouteWaves;
+constexpr int kQpThreads = kRouteThreads;
 
 template <int NCH, int BPL>
 __global__ __launch_bounds__(kQpThreads) void quantize_permute_kernel(
@@ -378,20 +377,16 @@ __global__ __launch_bounds__(kQpThreads) void quantize_permute_kernel(
     const int32_t* __restrict__ cnt, const int32_t* __restrict__ rank, int nchunks, int chunk_log,
     uint8_t* __restrict__ codes, uint8_t* __restrict__ bscales, float* __restrict__ rscales,
     int32_t* __restrict__ offsets, int32_t* __restrict__ row_to_tk, int32_t* __restrict__ tk_to_row) {
-  __shared__ int32_t sbase[2][NVFP4MOE_MAX_EXPERTS];   // first row of expert e in chunk c0, c0 + 1
-  __shared__ int32_t wsum[kQpWaves];
-  __shared__ int32_t tab[kCountTable];                  // the count table
-  const int lane = lane_id(), wave = threadIdx.x >> 6, tid = threadIdx.x;
+  __shared__ RouteLds lds;
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * kQpWaves + wave;
   const int e0 = (int)((int64_t)blockIdx.x * kQpWaves * k);       // first entry of the group
-  const int c0 = e0 >> chunk_log;                                  // its chunk
   const int n = (int)(T * k);                                      // routing entries (T >= 1)
-  const int ntab = nchunks * E;
 
   // every load first: the count table and this token's entries, then its activations
-  int tv[kCountTable / kQpThreads];             // the table, 8 independent loads per thread
-#pragma unroll
-  for (int u = 0; u < kCountTable / kQpThreads; ++u) tv[u] = cnt[min(u * kQpThreads + tid, ntab - 1)];
+  RouteTable table;
+  table.c0 = e0 >> chunk_log;
+  table.load(cnt, nchunks * E);
   const int my_i = (int)(t * k) + lane;
   const bool mine = t < T && lane < k;          // lane < k holds entry my_i of this token
   const int my_e = ids[min(my_i, n - 1)];
@@ -401,59 +396,12 @@ __global__ __launch_bounds__(kQpThreads) void quantize_permute_kernel(
   const int64_t tl = min(t, T - 1);
   if constexpr (kC) load_bf16_c<BPL>(x + tl * (int64_t)K, raw);
   else load_bf16_raw<NCH>(x + tl * (int64_t)K, K, raw);
-
-  // the table: per expert the total and the entries in chunks before c0, c0 + 1
-#pragma unroll
-  for (int u = 0; u < kCountTable / kQpThreads; ++u) {
-    const int i = u * kQpThreads + tid;
-    tab[i] = i < ntab ? tv[u] : 0;
-  }
-  lds_only_barrier();
-  int tot[kQpExp], b0[kQpExp], b1[kQpExp];
-#pragma unroll
-  for (int u = 0; u < kQpExp; ++u) { tot[u] = 0; b0[u] = 0; b1[u] = 0; }
-  for (int c = 0; c < nchunks; ++c) {
-#pragma unroll
-    for (int u = 0; u < kQpExp; ++u) {
-      const int e = kQpExp * tid + u;
-      const int v = e < E ? tab[c * E + e] : 0;
-      tot[u] += v;
-      if (c < c0) b0[u] += v;
-      if (c <= c0) b1[u] += v;
-    }
-  }
-  // expert offsets: exclusive scan of the totals over experts
-  int mine_tot = 0;
-#pragma unroll
-  for (int u = 0; u < kQpExp; ++u) mine_tot += tot[u];
-  int incl = mine_tot;
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const int y = __shfl_up(incl, off, kWave);
-    if (lane >= off) incl += y;
-  }
-  if (lane == kWave - 1) wsum[wave] = incl;
-  lds_only_barrier();
-  int before = 0;
-  for (int w = 0; w < wave; ++w) before += wsum[w];
-  int off_e = before + incl - mine_tot;   // offset of expert kQpExp * tid
-#pragma unroll
-  for (int u = 0; u < kQpExp; ++u) {
-    const int e = kQpExp * tid + u;
-    if (e < E) {
-      sbase[0][e] = off_e + b0[u];
-      sbase[1][e] = off_e + b1[u];
-      if (blockIdx.x == 0) offsets[e] = off_e;
-    }
-    off_e += tot[u];
-  }
-  if (blockIdx.x == 0 && tid == kQpThreads - 1) offsets[E] = before + incl;
-  lds_only_barrier();
+  table.scan(lds, nchunks, E, offsets);
   if (t >= T) return;
   // the rows of this token's entries (a rank >= 0 marks a valid expert id)
   int row = -1;
   if (mine) {
-    if (my_r >= 0) row = sbase[(my_i >> chunk_log) - c0][my_e] + my_r;
+    if (my_r >= 0) row = lds.first[(my_i >> chunk_log) - table.c0][my_e] + my_r;
     tk_to_row[my_i] = row;
     if (row >= 0) row_to_tk[row] = my_i;
   }

@@ -156,4 +156,82 @@ static __global__ __launch_bounds__(kPlanThreads) void route_scan_kernel(
   if (tid == kPlanThreads - 1) offsets[E] = wbefore + incl;
 }
 
+// What a main pass of 512-thread workgroups, each owning kRouteTokens consecutive tokens, makes of the count
+// table: load() issues the table's loads (unconditional, indices clamped into it), scan() turns it into the
+// expert offsets (written by workgroup 0) and, in LDS, the first row of every expert in the chunk of the
+// workgroup's first entry and in the next one; its barriers order LDS alone, so that loads issued in between
+// stay in flight.  Needs nchunks * E <= kCountTable.
+constexpr int kRouteTokens = 8;
+constexpr int kRouteThreads = 512;
+constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kRouteExp = NVFP4MOE_MAX_EXPERTS / kRouteThreads;   // experts per thread (2)
+static_assert(kRouteTokens * NVFP4MOE_MAX_TOPK <= 1 << kPlanChunkLogMin, "a workgroup's entries lie in at most two chunks");
+
+struct RouteLds {
+  int32_t first[2][NVFP4MOE_MAX_EXPERTS];   // first row of expert e in chunk c0, c0 + 1
+  int32_t wsum[kRouteWaves];
+  int32_t tab[kCountTable];
+};
+
+struct RouteTable {
+  int tv[kCountTable / kRouteThreads];      // 8 independent loads per thread
+  int c0;                                   // the chunk of the workgroup's first entry
+
+  __device__ __forceinline__ void load(const int32_t* __restrict__ cnt, int ntab) {
+#pragma unroll
+    for (int u = 0; u < kCountTable / kRouteThreads; ++u)
+      tv[u] = cnt[min(u * kRouteThreads + (int)threadIdx.x, ntab - 1)];
+  }
+
+  __device__ __forceinline__ void scan(RouteLds& s, int nchunks, int E, int32_t* __restrict__ offsets) {
+    const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, ntab = nchunks * E;
+#pragma unroll
+    for (int u = 0; u < kCountTable / kRouteThreads; ++u) {
+      const int i = u * kRouteThreads + tid;
+      s.tab[i] = i < ntab ? tv[u] : 0;
+    }
+    lds_only_barrier();
+    int tot[kRouteExp], b0[kRouteExp], b1[kRouteExp];
+#pragma unroll
+    for (int u = 0; u < kRouteExp; ++u) { tot[u] = 0; b0[u] = 0; b1[u] = 0; }
+    for (int c = 0; c < nchunks; ++c) {
+#pragma unroll
+      for (int u = 0; u < kRouteExp; ++u) {
+        const int e = kRouteExp * tid + u;
+        const int v = e < E ? s.tab[c * E + e] : 0;
+        tot[u] += v;
+        if (c < c0) b0[u] += v;
+        if (c <= c0) b1[u] += v;
+      }
+    }
+    // expert offsets: exclusive scan of the totals over experts
+    int mine_tot = 0;
+#pragma unroll
+    for (int u = 0; u < kRouteExp; ++u) mine_tot += tot[u];
+    int incl = mine_tot;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int y = __shfl_up(incl, off, kWave);
+      if (lane >= off) incl += y;
+    }
+    if (lane == kWave - 1) s.wsum[wave] = incl;
+    lds_only_barrier();
+    int before = 0;
+    for (int w = 0; w < wave; ++w) before += s.wsum[w];
+    int off_e = before + incl - mine_tot;   // offset of expert kRouteExp * tid
+#pragma unroll
+    for (int u = 0; u < kRouteExp; ++u) {
+      const int e = kRouteExp * tid + u;
+      if (e < E) {
+        s.first[0][e] = off_e + b0[u];
+        s.first[1][e] = off_e + b1[u];
+        if (blockIdx.x == 0) offsets[e] = off_e;
+      }
+      off_e += tot[u];
+    }
+    if (blockIdx.x == 0 && tid == kRouteThreads - 1) offsets[E] = before + incl;
+    lds_only_barrier();
+  }
+};
+
 }  // namespace nvfp4moe

@@ -228,7 +228,7 @@ def test_refusals():
     with pytest.raises(TypeError):
         pmg.moe_permute(x, ids, 4, out={"rows": d.bfloat16()})
     with pytest.raises(pmg.NVFP4Error, match="workspace"):
-        pmg.moe_permute(x, ids, 4, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        pmg.moe_permute(None, ids.repeat(2000, 1), 4, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(pmg.NVFP4Error):
         pmg.moe_permute(torch.zeros(4, 12, device="cuda"), ids, 4)
     with pytest.raises(ValueError, match="T \\* k"):
