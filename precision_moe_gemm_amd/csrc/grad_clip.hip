@@ -32,7 +32,6 @@ constexpr int kPiece = 65536;         // bytes of a piece, 16-byte words of one 
 constexpr int kPieceWords = kPiece / 16;
 constexpr int kPartials = 1024;       // norm workgroups over all launches (more where launches are more)
 constexpr int kAhead = 4;
-constexpr int64_t kCached = 256ll << 20;   // bytes of tensors from which on they are streamed
 
 struct Table {
   const void* in[kTensors];
@@ -92,18 +91,6 @@ __device__ __forceinline__ double squares(uint4 v, double acc) {
   return acc;
 }
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-template <bool STREAM>
-__device__ __forceinline__ uint4 load_word(const uint4* p) {
-  if constexpr (STREAM) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
-  else return *p;
-}
-template <bool STREAM>
-__device__ __forceinline__ void store_word(uint4* p, uint4 v) {
-  if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
-  else *p = v;
-}
-
 template <bool F32, bool STREAM>
 __device__ __forceinline__ double piece_squares(const void* p, int64_t numel, const Piece& q) {
   constexpr int V = F32 ? 4 : 8;
@@ -113,7 +100,7 @@ __device__ __forceinline__ double piece_squares(const void* p, int64_t numel, co
   for (; w + (kAhead - 1) * kThreads < q.w1; w += kAhead * kThreads) {
     uint4 r[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) r[u] = load_word<STREAM>(words + w + u * kThreads);
+    for (int u = 0; u < kAhead; ++u) r[u] = load16<STREAM>(words + w + u * kThreads);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) part[u] = squares<F32>(r[u], part[u]);
   }
@@ -184,7 +171,7 @@ __device__ __forceinline__ void scale_piece(const void* in, void* out, int64_t n
     for (int64_t w0 = q.w0 + threadIdx.x; w0 < q.w1; w0 += kAhead * kThreads) {
       uint4 r[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) r[u] = load_word<STREAM>(src + min(w0 + u * kThreads, q.w1 - 1));
+      for (int u = 0; u < kAhead; ++u) r[u] = load16<STREAM>(src + min(w0 + u * kThreads, q.w1 - 1));
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         if (w0 + u * kThreads >= q.w1) continue;
@@ -194,7 +181,7 @@ __device__ __forceinline__ void scale_piece(const void* in, void* out, int64_t n
           if constexpr (F32) x[j] = __float_as_uint(times(__uint_as_float(x[j]), c));
           else x[j] = bf16x2_rne(times(bf16_lo(x[j]), c), times(bf16_hi(x[j]), c));
         }
-        store_word<STREAM>(dst + w0 + u * kThreads, make_uint4(x[0], x[1], x[2], x[3]));
+        store16<STREAM>(dst + w0 + u * kThreads, make_uint4(x[0], x[1], x[2], x[3]));
       }
     }
   } else {
@@ -295,7 +282,7 @@ int run(const void* const* in, void* const* out, const int32_t* dtype, const int
   int used = 0;
   int64_t bytes = 0;
   for (int i = 0; i < n; ++i) bytes += numel[i] * (dtype[i] == NVFP4_IN_F32 ? 4 : 2);
-  const bool stream = bytes >= kCached;
+  const bool stream = bytes >= kLastLevelCache;
   for (int i = 0; i < n;) {
     i = fill(t, in, out, dtype, numel, i, n);
     if (!t.n) break;

@@ -18,10 +18,7 @@ constexpr int kCols = 512;      // elements of a row that a wavefront takes at a
 // product that reads them next gains less from their being cached than that: permutation and a BF16 gate_up
 // product together take 169 us for 176 at 600 tokens, 202 for 201 at 2048, 247 for 249 at 4096, 361 for 381
 // at 8192.
-__device__ __forceinline__ void store_row(uint4* dst, uint4 v) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(dst));
-}
+__device__ __forceinline__ void store_row(uint4* dst, uint4 v) { store16<true>(dst, v); }
 
 // A wavefront's part of a token's row: its first kHeld 16-byte words a lane stay in registers (rows up to
 // 4 KB), requested before the routing is known; longer rows are read again for what lies behind.
@@ -193,7 +190,8 @@ __global__ __launch_bounds__(kRouteThreads) void permute_short_kernel(
 }
 
 // One wavefront per 512 columns of a token's sum, taken in FP32 and in slot order with products and sums
-// rounded apart; the loads of 8 slots are issued before the first is added.
+// rounded apart; the loads of 8 slots are issued before the first is added.  They are non-temporal: each row
+// is read once (4096 tokens x 8 rows of 2048 bf16: 27 us for 29; 151 MB, so 5.6 TB/s).
 template <bool DF32, bool YF32>
 __global__ __launch_bounds__(kWaves * 64) void combine_kernel(
     const void* __restrict__ d, int64_t T, int k, int H, const int32_t* __restrict__ tk_to_row,
@@ -218,7 +216,7 @@ __global__ __launch_bounds__(kWaves * 64) void combine_kernel(
       const int row = __shfl(my_row, s0 + u, kWave);   // s0 + u < 40: a lane; entries past k have no row
       ws[u] = __shfl(my_w, s0 + u, kWave);
       ok[u] = row >= 0 && row < T * k && inside;
-      if (ok[u]) raw[u] = load8<DF32>(d, (int64_t)row * H + c);
+      if (ok[u]) raw[u] = load8<DF32, true>(d, (int64_t)row * H + c);
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -239,9 +237,12 @@ __global__ __launch_bounds__(kWaves * 64) void combine_kernel(
 // One wavefront per entry i = (t, s): dd[row] = w_i dy[t], dw_i = <dy[t], d[row]> in FP32, added within
 // the lane and then over the wavefront in a fixed order.  An entry without a row has dw_i = 0.  The loads of
 // kAhead pieces of 512 columns are issued before the first is used (4096 tokens x 8 rows of 2048 bf16: 58 us
-// with 4, 65 with 2, 70 with 1; 285 MB, so 4.9 TB/s); the token's k wavefronts share dy[t] in the caches.
+// with 4, 65 with 2, 70 with 1); the token's k wavefronts share dy[t] in the caches.  STREAM, where the
+// operands do not fit the last-level cache: d and dd are non-temporal (54 us for 58; 285 MB, so 5.3 TB/s;
+// with the BF16 input-gradient product that reads dd next 256 us for 263, 377 for 390 at 8192 tokens, but 206
+// for 203 at 2048 and 166 for 162 at 512, where the caches hold them).
 constexpr int kAhead = 4;
-template <bool YF32, bool DF32>
+template <bool YF32, bool DF32, bool STREAM>
 __global__ __launch_bounds__(kWaves * 64) void combine_backward_kernel(
     const void* __restrict__ dy, const void* __restrict__ d, int64_t R, int k, int H,
     const int32_t* __restrict__ tk_to_row, const float* __restrict__ topk_w, void* __restrict__ dd,
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(kWaves * 64) void combine_backward_kernel(
       for (int u = 0; u < kAhead; ++u) {
         const int c = min(c0 + u * kCols, H - 8);
         yr[u] = load8<YF32>(dy, t * H + c);
-        if (dw) dr[u] = load8<DF32>(d, row * H + c);
+        if (dw) dr[u] = load8<DF32, STREAM>(d, row * H + c);
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(kWaves * 64) void combine_backward_kernel(
         if (dd) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = w * y[j];
-          store8<DF32>(dd, row * H + c, v);
+          store8<DF32, STREAM>(dd, row * H + c, v);
         }
       }
     }
@@ -383,10 +384,14 @@ NVFP4MOE_API int moe_combine_backward(const void* dy, int32_t dy_dtype, const vo
   const int64_t R = T * (int64_t)k;
   const unsigned grid = (unsigned)((R + mp::kWaves - 1) / mp::kWaves);
   const bool yf = dy_dtype == NVFP4_IN_F32, df = d_dtype == NVFP4_IN_F32;
-#define MP_BACKWARD(Y, D) \
-  mp::combine_backward_kernel<Y, D><<<grid, mp::kWaves * 64, 0, s>>>(dy, d, R, k, (int)H, tk_to_row, topk_w, dd, dtopk_w)
-  if (yf) df ? MP_BACKWARD(true, true) : MP_BACKWARD(true, false);
-  else df ? MP_BACKWARD(false, true) : MP_BACKWARD(false, false);
+  const int64_t bytes = T * H * (yf ? 4 : 2) + R * H * (df ? 4 : 2) * ((dtopk_w ? 1 : 0) + (dd ? 1 : 0));
+  const bool stream_out = bytes >= kLastLevelCache;
+#define MP_BACKWARD(Y, D, S) \
+  mp::combine_backward_kernel<Y, D, S><<<grid, mp::kWaves * 64, 0, s>>>(dy, d, R, k, (int)H, tk_to_row, topk_w, dd, dtopk_w)
+#define MP_BACKWARD_BY(Y, D) (stream_out ? MP_BACKWARD(Y, D, true) : MP_BACKWARD(Y, D, false))
+  if (yf) df ? MP_BACKWARD_BY(true, true) : MP_BACKWARD_BY(true, false);
+  else df ? MP_BACKWARD_BY(false, true) : MP_BACKWARD_BY(false, false);
+#undef MP_BACKWARD_BY
 #undef MP_BACKWARD
   return launch_status();
 }

@@ -6,6 +6,23 @@
 
 namespace nvfp4moe {
 
+constexpr int64_t kLastLevelCache = 256ll << 20;   // bytes
+
+// 16 bytes; STREAM: non-temporal, for data that the caches would not hold until it is used again
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <bool STREAM>
+__device__ __forceinline__ uint4 load16(const void* p) {
+  const u32x4* q = static_cast<const u32x4*>(p);
+  if constexpr (STREAM) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(q));
+  else return __builtin_bit_cast(uint4, *q);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(void* p, uint4 v) {
+  u32x4* q = static_cast<u32x4*>(p);
+  if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), q);
+  else *q = __builtin_bit_cast(u32x4, v);
+}
+
 template <bool F32>
 __device__ __forceinline__ float load_one(const void* p, int64_t i) {
   if constexpr (F32) return static_cast<const float*>(p)[i];
@@ -23,12 +40,12 @@ __device__ __forceinline__ void store_one(void* p, int64_t i, float v) {
 template <bool F32>
 struct Raw8 { uint4 q[F32 ? 2 : 1]; };
 
-template <bool F32>
+template <bool F32, bool STREAM = false>
 __device__ __forceinline__ Raw8<F32> load8(const void* p, int64_t i) {
   Raw8<F32> r;
-  const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (F32 ? 4 : 2));
+  const char* s = static_cast<const char*>(p) + i * (F32 ? 4 : 2);
 #pragma unroll
-  for (int j = 0; j < (F32 ? 2 : 1); ++j) r.q[j] = s[j];
+  for (int j = 0; j < (F32 ? 2 : 1); ++j) r.q[j] = load16<STREAM>(s + 16 * j);
   return r;
 }
 
@@ -46,15 +63,17 @@ __device__ __forceinline__ void unpack8(const Raw8<F32>& r, float (&v)[8]) {
 }
 
 // bf16: each value rounded to nearest even
-template <bool F32>
+template <bool F32, bool STREAM = false>
 __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
   if constexpr (F32) {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    d[0] = make_float4(v[0], v[1], v[2], v[3]);
-    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    float* d = static_cast<float*>(p) + i;
+#pragma unroll
+    for (int j = 0; j < 8; j += 4)
+      store16<STREAM>(d + j, make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
+                                        __float_as_uint(v[j + 3])));
   } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-        make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+    store16<STREAM>(static_cast<uint16_t*>(p) + i, make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
+                                                              bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])));
   }
 }
 
