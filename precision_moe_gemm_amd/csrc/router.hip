@@ -1,9 +1,12 @@
 // The router's choice (top-k experts of each token and their weights) and its gradient, for gfx950.
 //
 // A group of G lanes takes a token: G = 16 (four tokens a wavefront) up to 256 experts, the whole wavefront
-// above.  Each lane holds NE consecutive logits, read as vectors wherever the row starts.  Both kernels are
-// bound by the issue of vector instructions rather than by the row's bytes, and a round of the choice costs
-// a group's reduction whatever the group's size, so that more tokens share it in the narrow groups.
+// above.  Each lane holds NE consecutive logits, read as vectors wherever the row starts.  A round of the
+// choice costs a group's reduction whatever the group's size, so that more tokens share it in the narrow
+// groups: 16381 x 250 bf16 logits, k = 6, take 6.6 us for 13.7 with a wavefront a token (8.2 MB read: 1.6 us
+// at a copy's rate), the gradient 8.3 for 11.8 (16.4 MB).  Of these a launch of one token takes 3.5 and 2.4,
+// the chain of its loads, rounds and stores; all the wavefronts of the larger case are resident at once and
+// run little more than one such chain.  (A shorter exp made no difference.)
 #include "common.h"
 #include "fp8.h"
 #include "rows.h"
@@ -207,61 +210,77 @@ __global__ __launch_bounds__(kThreads) void topk_kernel(const void* __restrict__
 // The logits' gradient from the weights' g: with mean = sum_s w_s g_s over the token's entries,
 //   renorm: dl_e = sum over the entries s of e of w_s (g_s - mean), 0 for an expert that was not chosen;
 //   else    dl_e = p_e (sum over the entries s of e of g_s - mean), p = softmax of the row.
-// The sum over an expert's entries (one, from a router) is formed in slot order by the first of them, and
-// goes to the lane that holds the expert through the row's line in LDS.
+// An expert's sum goes to the lane that holds the expert through the row's line in LDS (a word of padding a
+// lane keeps the lanes' words in different banks).  Each entry first leaves its number there: one that reads
+// another's back shares its expert, and then the sums over equal experts are formed, in slot order, by the
+// first entry of each; a router's choices are all different, and their sums the entries' own.
 template <int NE, int G, bool F32>
 __global__ __launch_bounds__(kThreads) void topk_backward_kernel(
     const void* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ w,
     const float* __restrict__ dw, int64_t T, int E, int k, int renorm, void* __restrict__ dlogits) {
   constexpr int kSlots = (NVFP4MOE_MAX_TOPK + G - 1) / G;
-  __shared__ float lines[kThreads / G][NE * G];
+  constexpr int kLine = NE * G + G;
+  __shared__ float lines[kThreads / G][kLine];
   const int64_t row = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G;
   const int64_t t = min(row, T - 1);
   const int g = threadIdx.x % G, from = window<NE>(g, E);
   float* line = lines[threadIdx.x / G];
+  const auto at = [](int e) { return e + e / NE; };
   float v[NE];
   if (!renorm) load_logits<NE, F32>(logits, t * E + from, v);
   int id[kSlots];
-  float ws[kSlots], x[kSlots], mean = 0.0f;
+  float x[kSlots], ws[kSlots];
 #pragma unroll
   for (int u = 0; u < kSlots; ++u) {
-    const int s = u * G + g;
-    id[u] = s < k ? ids[t * k + s] : -1;
-    ws[u] = x[u] = 0.0f;
-    if (id[u] >= 0 && id[u] < E) { ws[u] = w[t * k + s]; x[u] = dw[t * k + s]; }
-    else id[u] = -1;
-    mean += ws[u] * x[u];
+    const int64_t i = t * k + min(u * G + g, k - 1);
+    id[u] = ids[i];
+    ws[u] = w[i];
+    x[u] = dw[i];
   }
 #pragma unroll
-  for (int j = 0; j < NE; ++j) line[j * G + g] = 0.0f;
+  for (int j = 0; j < kLine; j += G) line[j + g] = 0.0f;
   __syncthreads();
+  float mean = 0.0f;
+#pragma unroll
+  for (int u = 0; u < kSlots; ++u) {
+    if (u * G + g >= k || id[u] < 0 || id[u] >= E) { id[u] = -1; ws[u] = x[u] = 0.0f; }
+    mean += ws[u] * x[u];
+    if (id[u] >= 0) line[at(id[u])] = __int_as_float(u * G + g);
+  }
   mean = group_sum<G>(mean);
+  __syncthreads();
   float total[kSlots];
-  bool first[kSlots];
+  bool first[kSlots], shared = false;
 #pragma unroll
   for (int u = 0; u < kSlots; ++u) {
     if (renorm) x[u] = ws[u] * (x[u] - mean);
-    total[u] = 0.0f;
+    total[u] = x[u];
     first[u] = id[u] >= 0;
+    shared |= first[u] && __float_as_int(line[at(id[u])]) != u * G + g;
   }
-  for (int q = 0; q < k; ++q) {
-    const bool hi = q >= G;
-    const int e = __shfl(hi ? id[kSlots - 1] : id[0], q % G, G);
-    const float y = __shfl(hi ? x[kSlots - 1] : x[0], q % G, G);
+  if (__ballot(shared)) {
 #pragma unroll
-    for (int u = 0; u < kSlots; ++u) {
-      if (e != id[u]) continue;
-      total[u] += y;
-      if (q < u * G + g) first[u] = false;
+    for (int u = 0; u < kSlots; ++u) total[u] = 0.0f;
+    for (int q = 0; q < k; ++q) {
+      const bool hi = q >= G;
+      const int e = __shfl(hi ? id[kSlots - 1] : id[0], q % G, G);
+      const float y = __shfl(hi ? x[kSlots - 1] : x[0], q % G, G);
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u) {
+        if (e != id[u]) continue;
+        total[u] += y;
+        if (q < u * G + g) first[u] = false;
+      }
     }
   }
+  __syncthreads();
 #pragma unroll
   for (int u = 0; u < kSlots; ++u)
-    if (first[u]) line[id[u]] = total[u];
+    if (first[u]) line[at(id[u])] = total[u];
   __syncthreads();
   float d[NE];
 #pragma unroll
-  for (int j = 0; j < NE; ++j) d[j] = line[from + j];
+  for (int j = 0; j < NE; ++j) d[j] = line[at(from + j)];
   if (!renorm) {
     float m = v[0];
 #pragma unroll
