@@ -598,7 +598,7 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  *   entry whose id is outside [0, E) is left out.  logits are read only with renorm 0 (NULL
  *   otherwise).  Every element of dlogits is written.
  * Both require 1 <= k <= min(E, NVFP4MOE_MAX_TOPK), E <= NVFP4MOE_MAX_EXPERTS,
- * T * k <= INT32_MAX / 2.
+ * T * k <= MOE_MAX_ROWS.
  *
  * moe_permute - nvfp4_quantize_permute's routing for rows that are not quantised here:
  * expert_offsets, row_to_tk and tk_to_row exactly as it writes them, and
@@ -607,7 +607,8 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  *   workspace: moe_permute_workspace_size(T, k, E) bytes (0 for short routing lists: NULL),
  *   used as nvfp4_quantize_permute uses its own; dev_err as there
  * rows and row_to_tk at or beyond expert_offsets[E] are left as they were.  Requires
- * H % 8 == 0, 8 <= H <= MOE_MAX_H and the routing limits of nvfp4_quantize_permute.
+ * H % 8 == 0, 8 <= H <= MOE_MAX_H, 1 <= k <= min(E, NVFP4MOE_MAX_TOPK), 1 <= E <=
+ * NVFP4MOE_MAX_EXPERTS, T * k <= MOE_MAX_ROWS.
  * Its gradient is moe_combine without weights.
  *
  * moe_combine - y[t] = sum_s w_s d[tk_to_row[t*k+s]]: unpermute_combine for either type of
@@ -621,14 +622,14 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  *   dy [T][H] of dy_dtype; d and dd [T*k][H] of d_dtype; dtopk_w float [T*k].  dd or
  *   dtopk_w may be NULL (not computed), d too without dtopk_w.  Rows that no entry names
  *   are left as they were.  tk_to_row names each row at most once.
- * The three require H % 8 == 0, 8 <= H <= MOE_MAX_H, 1 <= k <= NVFP4MOE_MAX_TOPK,
- * T * k <= INT32_MAX / 2.
+ * Both require H % 8 == 0, 8 <= H <= MOE_MAX_H, 1 <= k <= NVFP4MOE_MAX_TOPK, T * k <=
+ * MOE_MAX_ROWS, and moe_combine T * ceil(H / 512) <= MOE_MAX_ROWS.
  *
  * swiglu_backward_weights - swiglu_backward (the same dgu, bit for bit) with the gradient of
  * the router weights that the SwiGLU applies:
  *     dtopk_w[row_to_tk[r]] = sum_j dh[r][j] silu(g[r][j]) u[r][j]   in FP64, rounded once
  *   tk_to_row int32 [R_cap], the inverse map: entries without a row have 0.  Arguments and
- *   requirements otherwise as swiglu_backward with topk_w; R_cap <= INT32_MAX / 2.
+ *   requirements otherwise as swiglu_backward with topk_w; R_cap <= MOE_MAX_ROWS.
  *
  * moe_grad_norm - norm = sqrt(sum of x^2 over the elements of n tensors), summed in FP64 in
  * a fixed order and rounded once to float.
@@ -642,11 +643,12 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  * pointers; out_j is grads_j itself (in place) or memory that overlaps no other tensor of
  * the call (NVFP4_ERR_ARG).  A norm that is inf gives c = 0, a NaN one c = NaN.
  * Requires max_norm >= 0 (inf: the norm alone, and a copy where not in place),
- * n <= MOE_MAX_TENSORS, numel <= MOE_MAX_NUMEL.
+ * n <= MOE_MAX_TENSORS and at most MOE_MAX_GRAD_BYTES bytes of tensors.
  */
+#define MOE_MAX_ROWS ((1 << 26) - 16)   /* T * k: what one launch holds */
 #define MOE_MAX_H (1 << 20)
 #define MOE_MAX_TENSORS 65536
-#define MOE_MAX_NUMEL (1ll << 38)
+#define MOE_MAX_GRAD_BYTES (1ll << 39)
 NVFP4MOE_API int moe_router_topk(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k,
                                  int32_t renorm, int32_t* topk_ids, float* topk_w, void* stream);
 NVFP4MOE_API int moe_router_topk_backward(const void* logits, int32_t dtype, const int32_t* topk_ids,

@@ -305,7 +305,7 @@ NVFP4MOE_API int swiglu_backward_weights(const float* gu, const float* dh, int64
                                          const int32_t* expert_offsets, int32_t E, const float* topk_w,
                                          const int32_t* row_to_tk, const int32_t* tk_to_row, uint16_t* dgu,
                                          float* dtopk_w, void* stream) {
-  if (R_cap < 0 || R_cap > INT32_MAX / 2 || I <= 0 || I % 8 != 0 || I > INT32_MAX / 4) return NVFP4_ERR_SHAPE;
+  if (R_cap < 0 || R_cap > MOE_MAX_ROWS || I <= 0 || I % 8 != 0 || I > INT32_MAX / 4) return NVFP4_ERR_SHAPE;
   if (E < 1 || E > NVFP4MOE_MAX_EXPERTS) return NVFP4_ERR_SHAPE;
   if (R_cap == 0) return NVFP4_OK;
   if (!gu || !dh || !expert_offsets || !topk_w || !row_to_tk || !tk_to_row || !dgu || !dtopk_w) return NVFP4_ERR_NULL;

@@ -220,9 +220,12 @@ inline int blocks_each(int64_t n) { return std::max(1, kPartials / std::max(1, l
 int check(const void* const* in, const int32_t* dtype, const int64_t* numel, int32_t n) {
   if (n < 0 || n > MOE_MAX_TENSORS) return NVFP4_ERR_SHAPE;
   if (n && (!in || !dtype || !numel)) return NVFP4_ERR_NULL;
+  int64_t bytes = 0;
   for (int i = 0; i < n; ++i) {
     if (dtype[i] != NVFP4_IN_BF16 && dtype[i] != NVFP4_IN_F32) return NVFP4_ERR_ARG;
-    if (numel[i] < 0 || numel[i] > MOE_MAX_NUMEL) return NVFP4_ERR_SHAPE;
+    if (numel[i] < 0 || numel[i] > MOE_MAX_GRAD_BYTES) return NVFP4_ERR_SHAPE;
+    bytes += numel[i] * (dtype[i] == NVFP4_IN_F32 ? 4 : 2);
+    if (bytes > MOE_MAX_GRAD_BYTES) return NVFP4_ERR_SHAPE;
     if (numel[i] && !in[i]) return NVFP4_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(in[i]) & (dtype[i] == NVFP4_IN_F32 ? 3 : 1)) return NVFP4_ERR_ALIGN;
   }
@@ -255,7 +258,8 @@ int overlaps(const void* const* in, void* const* out, const int32_t* dtype, cons
 }
 
 // Tensors [i0, n) into a table until it is full; returns the first that is not in it.  Empty tensors are
-// left out.  (kTensors tensors of MOE_MAX_NUMEL elements have fewer than 2^31 - 2^11 pieces.)
+// left out.  (MOE_MAX_GRAD_BYTES and MOE_MAX_TENSORS
+// make fewer than 2^24 pieces, as many workgroups of 256 threads as a launch holds.)
 int fill(Table& t, const void* const* in, void* const* out, const int32_t* dtype, const int64_t* numel, int i0, int n) {
   t.n = 0;
   t.first[0] = 0;

@@ -294,7 +294,7 @@ inline bool type_ok(int32_t t) { return t == NVFP4_IN_BF16 || t == NVFP4_IN_F32;
 
 inline int check(int64_t T, int32_t k, int64_t H) {
   if (T < 0 || k < 1 || k > NVFP4MOE_MAX_TOPK || H < 8 || H % 8 != 0 || H > MOE_MAX_H) return NVFP4_ERR_SHAPE;
-  return T * (int64_t)k > INT32_MAX / 2 ? NVFP4_ERR_SHAPE : NVFP4_OK;
+  return T > MOE_MAX_ROWS || T * (int64_t)k > MOE_MAX_ROWS ? NVFP4_ERR_SHAPE : NVFP4_OK;
 }
 
 }  // namespace mp
@@ -353,13 +353,13 @@ NVFP4MOE_API int moe_combine(const void* d, int32_t d_dtype, int64_t T, int32_t 
                              const float* topk_w, void* y, int32_t y_dtype, void* stream) {
   if (!mp::type_ok(d_dtype) || !mp::type_ok(y_dtype)) return NVFP4_ERR_ARG;
   if (const int bad = mp::check(T, k, H)) return bad;
+  const int64_t items = T * ((H + mp::kCols - 1) / mp::kCols);
+  if (items > MOE_MAX_ROWS) return NVFP4_ERR_SHAPE;
   if (T == 0) return NVFP4_OK;
   if (!d || !tk_to_row || !y) return NVFP4_ERR_NULL;
   if (!aligned16(d) || !aligned16(tk_to_row) || !aligned16(topk_w) || !aligned16(y)) return NVFP4_ERR_ALIGN;
   if (d == y) return NVFP4_ERR_ARG;
-  const int64_t items = T * ((H + mp::kCols - 1) / mp::kCols);
   const int64_t grid = (items + mp::kWaves - 1) / mp::kWaves;
-  if (grid > INT32_MAX) return NVFP4_ERR_SHAPE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool df = d_dtype == NVFP4_IN_F32, yf = y_dtype == NVFP4_IN_F32;
 #define MP_COMBINE(D, Y) mp::combine_kernel<D, Y><<<(unsigned)grid, mp::kWaves * 64, 0, s>>>(d, T, k, (int)H, tk_to_row, topk_w, y)

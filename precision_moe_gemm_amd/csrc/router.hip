@@ -303,8 +303,7 @@ inline int check(int64_t T, int32_t E, int32_t k, int32_t dtype, int32_t renorm)
   if (dtype != NVFP4_IN_BF16 && dtype != NVFP4_IN_F32) return NVFP4_ERR_ARG;
   if (renorm != 0 && renorm != 1) return NVFP4_ERR_ARG;
   if (T < 0 || E < 1 || E > NVFP4MOE_MAX_EXPERTS || k < 1 || k > E || k > NVFP4MOE_MAX_TOPK) return NVFP4_ERR_SHAPE;
-  if (T * (int64_t)k > INT32_MAX / 2) return NVFP4_ERR_SHAPE;
-  return NVFP4_OK;
+  return T > MOE_MAX_ROWS || T * (int64_t)k > MOE_MAX_ROWS ? NVFP4_ERR_SHAPE : NVFP4_OK;
 }
 
 }  // namespace router

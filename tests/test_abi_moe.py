@@ -21,7 +21,7 @@ def test_router(lib):
     for f in (fwd, bwd):
         for kw in ({"dt": 2}, {"dt": -1}, {"rn": 2}, {"rn": -1}):
             assert f(**kw) == ERR_ARG, kw
-        for kw in ({"T": -1}, {"E": 0}, {"E": 1025}, {"k": 0}, {"k": 17}, {"E": 64, "k": 33}, {"T": 1 << 29}):
+        for kw in ({"T": -1}, {"E": 0}, {"E": 1025}, {"k": 0}, {"k": 17}, {"E": 64, "k": 33}, {"T": 1 << 24}, {"T": 1 << 26, "k": 1}, {"T": 1 << 62}):
             assert f(**kw) == ERR_SHAPE, kw
         for n in ("ids", "w"):
             assert f(**{n: None}) == ERR_NULL, n
@@ -43,7 +43,7 @@ def test_permute(lib):
                                      kw.get("r2t", P), kw.get("t2r", P), kw.get("ws", P), kw.get("wsb", size), None, None)
     assert f(dt=2) == ERR_ARG and f(rows=P) == ERR_ARG
     for kw in ({"T": -1}, {"H": 0}, {"H": 12}, {"H": (1 << 20) + 8}, {"k": 0}, {"k": 33}, {"k": 9, "E": 8}, {"E": 0},
-               {"E": 1025}, {"T": 1 << 27, "wsb": 1 << 40}):
+               {"E": 1025}, {"T": 1 << 23, "wsb": 1 << 40}, {"T": 1 << 62, "wsb": 1 << 40}):
         assert f(**kw) == ERR_SHAPE, kw
     for n in ("ids", "off", "r2t", "t2r", "ws", "x", "rows"):
         assert f(**{n: None}) == ERR_NULL, n
@@ -57,7 +57,8 @@ def test_combine(lib):
                                      kw.get("map", P), kw.get("w", P), kw.get("y", Q), kw.get("yd", 0), None)
     for kw in ({"dd": 2}, {"yd": 2}, {"y": P}):
         assert f(**kw) == ERR_ARG, kw
-    for kw in ({"T": -1}, {"T": 1 << 29}, {"k": 0}, {"k": 33}, {"H": 0}, {"H": 4}, {"H": 20}, {"H": (1 << 20) + 8}):
+    for kw in ({"T": -1}, {"T": 1 << 24}, {"T": 1 << 62}, {"T": 1 << 25, "k": 1, "H": 520}, {"k": 0}, {"k": 33}, {"H": 0}, {"H": 4},
+               {"H": 20}, {"H": (1 << 20) + 8}):
         assert f(**kw) == ERR_SHAPE, kw
     for n in ("d", "map", "y"):
         assert f(**{n: None}) == ERR_NULL, n
@@ -72,7 +73,7 @@ def test_combine_backward(lib):
         kw.get("map", P), kw.get("w", P), kw.get("dd", Q), kw.get("dw", Q), None)
     for kw in ({"yd": 2}, {"dt": 7}, {"dd": P}, {"dd": Q, "dy": Q}):
         assert f(**kw) == ERR_ARG, kw
-    for kw in ({"T": -1}, {"T": 1 << 29}, {"k": 0}, {"k": 33}, {"H": 0}, {"H": 20}, {"H": (1 << 20) + 8}):
+    for kw in ({"T": -1}, {"T": 1 << 24}, {"T": 1 << 62}, {"k": 0}, {"k": 33}, {"H": 0}, {"H": 20}, {"H": (1 << 20) + 8}):
         assert f(**kw) == ERR_SHAPE, kw
     for kw in ({"dy": None}, {"map": None}, {"d": None}, {"dd": None, "dw": None}):
         assert f(**kw) == ERR_NULL, kw
@@ -85,7 +86,7 @@ def test_swiglu_backward_weights(lib):
     f = lambda **kw: lib.swiglu_backward_weights(
         kw.get("gu", P), kw.get("dh", P), kw.get("R", 8), kw.get("I", 64), kw.get("off", P), kw.get("E", 4), kw.get("w", P),
         kw.get("r2t", P), kw.get("t2r", P), kw.get("dgu", P), kw.get("dw", Q), None)
-    for kw in ({"R": -1}, {"R": 1 << 30}, {"I": 0}, {"I": 12}, {"E": 0}, {"E": 1025}):
+    for kw in ({"R": -1}, {"R": 1 << 26}, {"I": 0}, {"I": 12}, {"E": 0}, {"E": 1025}):
         assert f(**kw) == ERR_SHAPE, kw
     for n in ("gu", "dh", "off", "w", "r2t", "t2r", "dgu", "dw"):
         assert f(**{n: None}) == ERR_NULL, n
@@ -118,7 +119,8 @@ def test_grad_norm_and_clip(lib):
         return got[0]
 
     assert call(n=-1) == ERR_SHAPE and call(n=65537) == ERR_SHAPE
-    assert call(((P, 1, -1),)) == ERR_SHAPE and call(((P, 1, (1 << 38) + 1),)) == ERR_SHAPE
+    assert call(((P, 1, -1),)) == ERR_SHAPE and call(((P, 1, (1 << 37) + 1),)) == ERR_SHAPE
+    assert call(((P, 0, 1 << 38), (Q, 1, 1))) == ERR_SHAPE and call(((P, 0, 1 << 62),)) == ERR_SHAPE
     assert call(((P, 2, 8),)) == ERR_ARG
     assert call(((None, 1, 8),)) == ERR_NULL
     assert call(((P + 2, 1, 8),)) == ERR_ALIGN and call(((P + 1, 0, 8),)) == ERR_ALIGN
