@@ -627,7 +627,7 @@ def _head(t, name, dtypes, ndim):
 def _give(t, name, shape, dtype, dtypes, like, dev):
     """An output: the caller's tensor, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     _arg(t, name, dtypes, dev, numel=math.prod(shape))
     return t
 

@@ -140,9 +140,10 @@ __global__ __launch_bounds__(256) void permute_gather_kernel(
 // sigmoid; silu = g * sigmoid), each output rounded once to bf16.  DW: also w's, the sum over the row of
 // dh * silu(g) * u in float64, rounded once to float32.  The wavefront of row r then also looks at entry r
 // and writes 0 for one that has no row, so that every entry of dw is written without a fill before.
-// STREAM, where the operands do not fit the last-level cache: gu and dh, which nothing else reads soon, are
-// read non-temporally (32768 rows of 768, 403 MB: 76 us for 78; with the BF16 input-gradient product that
-// reads dgu next 364 us for 371, 643 for 686 at twice the rows, but 232 for 229 at 4096 rows).
+// STREAM, where the operands do not fit the last-level cache: loads and stores are non-temporal (32768 rows of
+// 768, 403 MB: 77 us for 82; with the BF16 products that read dgu next the loads alone give 364 us for 371,
+// 643 for 686 at twice the rows, and the stores nothing more or less: 886 for 887, 1408 for 1405; at 4096
+// rows, which the caches hold, 232 for 229).
 template <bool DW, bool STREAM>
 __global__ __launch_bounds__(256) void swiglu_backward_kernel(
     const float* __restrict__ gu, const float* __restrict__ dh, int64_t R_cap, int I,
@@ -194,8 +195,8 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(
       og[j / 2] = bg[0] | (bg[1] << 16);
       ou[j / 2] = bu[0] | (bu[1] << 16);
     }
-    *reinterpret_cast<uint2*>(orow + base) = make_uint2(og[0], og[1]);
-    *reinterpret_cast<uint2*>(orow + I + base) = make_uint2(ou[0], ou[1]);
+    store8bytes<STREAM>(orow + base, make_uint2(og[0], og[1]));
+    store8bytes<STREAM>(orow + I + base, make_uint2(ou[0], ou[1]));
   }
   if (DW) {
     sum = wave_sum(sum);

@@ -23,6 +23,14 @@ __device__ __forceinline__ void store16(void* p, uint4 v) {
   else *q = __builtin_bit_cast(u32x4, v);
 }
 
+template <bool STREAM>
+__device__ __forceinline__ void store8bytes(void* p, uint2 v) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  u32x2* q = static_cast<u32x2*>(p);
+  if constexpr (STREAM) __builtin_nontemporal_store((u32x2){v.x, v.y}, q);
+  else *q = (u32x2){v.x, v.y};
+}
+
 template <bool F32>
 __device__ __forceinline__ float load_one(const void* p, int64_t i) {
   if constexpr (F32) return static_cast<const float*>(p)[i];
