@@ -2,6 +2,7 @@
 // gradient, for gfx950.  All are bound by memory: the sort reads every token row once and writes it k
 // times, the combine reads k rows for each that it writes, the gradient reads and writes k rows a token.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "route.h"
@@ -53,56 +54,119 @@ __device__ __forceinline__ void copy_to_rows(const Row& held, const uint4* __res
   }
 }
 
-// One wavefront per token, eight to a workgroup: the entries' rows from the count table and the ranks, the
-// maps, and the token's row copied to them.  The row is requested before the table is scanned.
-__global__ __launch_bounds__(kRouteThreads) void permute_kernel(
-    const uint4* __restrict__ x, int64_t T, int words, const int32_t* __restrict__ ids, int k, int E,
-    const int32_t* __restrict__ cnt, const int32_t* __restrict__ rank, int nchunks, int chunk_log,
-    uint4* __restrict__ rows, int32_t* __restrict__ offsets, int32_t* __restrict__ row_to_tk,
-    int32_t* __restrict__ tk_to_row) {
-  __shared__ RouteLds lds;
-  const int lane = lane_id();
-  const int64_t t = (int64_t)blockIdx.x * kRouteTokens + (threadIdx.x >> 6);
-  const int n = (int)(T * k);
-  RouteTable table;
-  table.c0 = (int)((int64_t)blockIdx.x * kRouteTokens * k) >> chunk_log;
-  table.load(cnt, nchunks * E);
-  const int i = (int)(t * k) + lane;
-  const int e = ids[min(i, n - 1)], r = rank[min(i, n - 1)];
-  const uint4* src = x + min(t, T - 1) * words;
-  Row held;
-  if (rows) held.load(src, words);
-  table.scan(lds, nchunks, E, offsets);
-  if (t >= T) return;
-  int row = -1;
-  if (lane < k) {
-    if (r >= 0) row = lds.first[(i >> chunk_log) - table.c0][e] + r;   // a rank marks a valid expert id
-    tk_to_row[i] = row;
-    if (row >= 0) row_to_tk[row] = i;
+// Long routing lists, whose count table no workgroup could scan: one wavefront-wide column of 64 experts per
+// workgroup, its 16 wavefronts a part of the chunks each.  table[c][e] becomes the entries of e in the chunks
+// before c, total[e] those of all.
+constexpr int kColumnWaves = 16;
+__global__ __launch_bounds__(kColumnWaves * 64) void route_columns_kernel(int32_t* __restrict__ table, int nchunks, int E,
+                                                                          int32_t* __restrict__ total) {
+  __shared__ int32_t part[kColumnWaves][kWave];
+  const int lane = lane_id(), wave = threadIdx.x >> 6, e = blockIdx.x * kWave + lane;
+  const int per = (nchunks + kColumnWaves - 1) / kColumnWaves;
+  const int lo = min(nchunks, wave * per), hi = min(nchunks, lo + per);
+  int sum = 0;
+  if (e < E)
+    for (int c = lo; c < hi; ++c) sum += table[(int64_t)c * E + e];
+  part[wave][lane] = sum;
+  __syncthreads();
+  if (e >= E) return;
+  int acc = 0;
+  for (int w = 0; w < wave; ++w) acc += part[w][lane];
+  if (wave == kColumnWaves - 1) total[e] = acc + sum;
+  for (int c = lo; c < hi; ++c) {
+    const int64_t at = (int64_t)c * E + e;
+    const int v = table[at];
+    table[at] = acc;
+    acc += v;
   }
-  if (rows) copy_to_rows(held, src, words, k, row, rows);
 }
 
-// The same from the first rows of route_scan_kernel: long routing lists.
-__global__ __launch_bounds__(kWaves * 64) void permute_rows_kernel(
-    const uint4* __restrict__ x, int64_t T, int words, const int32_t* __restrict__ ids, int k, int E,
-    const int32_t* __restrict__ base, const int32_t* __restrict__ rank, int chunk_log, uint4* __restrict__ rows,
-    int32_t* __restrict__ row_to_tk, int32_t* __restrict__ tk_to_row) {
-  const int64_t t = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (t >= T) return;
-  const int lane = lane_id();
-  const uint4* src = x + t * words;
-  Row held;
-  if (rows) held.load(src, words);
-  int row = -1;
-  if (lane < k) {
-    const int i = (int)(t * k) + lane;
-    const int r = rank[i];
-    if (r >= 0) row = base[(int64_t)(i >> chunk_log) * E + ids[i]] + r;
-    tk_to_row[i] = row;
-    if (row >= 0) row_to_tk[row] = i;
+// The expert offsets from the experts' totals, into LDS (and memory, from workgroup 0).
+__device__ __forceinline__ void scan_totals(const int32_t* __restrict__ total, int E, int32_t* __restrict__ first,
+                                            int32_t* __restrict__ wsum, int32_t* __restrict__ offsets) {
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
+  int tot[kRouteExp], sum = 0;
+#pragma unroll
+  for (int u = 0; u < kRouteExp; ++u) {
+    const int e = kRouteExp * tid + u;
+    tot[u] = e < E ? total[e] : 0;
+    sum += tot[u];
   }
-  if (rows) copy_to_rows(held, src, words, k, row, rows);
+  int incl = sum;
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int y = __shfl_up(incl, off, kWave);
+    if (lane >= off) incl += y;
+  }
+  if (lane == kWave - 1) wsum[wave] = incl;
+  __syncthreads();
+  int at = incl - sum;
+  for (int w = 0; w < wave; ++w) at += wsum[w];
+#pragma unroll
+  for (int u = 0; u < kRouteExp; ++u) {
+    const int e = kRouteExp * tid + u;
+    if (e < E) {
+      first[e] = at;
+      if (blockIdx.x == 0) offsets[e] = at;
+    }
+    at += tot[u];
+  }
+  if (blockIdx.x == 0 && tid == kRouteThreads - 1) offsets[E] = at;
+  __syncthreads();
+}
+
+// The main pass: `rounds` tokens to each of a workgroup's eight wavefronts, the entries' rows from their ranks
+// and from the count table (TABLE) or the columns' sums, the maps, and the token's row copied to them.  The
+// first token's row is requested before the table is scanned, each later one before the copies of the token
+// ahead of it.
+struct TotalsLds {
+  int32_t first[NVFP4MOE_MAX_EXPERTS], wsum[kRouteWaves];
+};
+template <bool TABLE>
+__global__ __launch_bounds__(kRouteThreads) void permute_kernel(
+    const uint4* __restrict__ x, int64_t T, int words, const int32_t* __restrict__ ids, int k, int E,
+    const int32_t* __restrict__ cnt, const int32_t* __restrict__ rank, const int32_t* __restrict__ total, int nchunks,
+    int chunk_log, int rounds, uint4* __restrict__ rows, int32_t* __restrict__ offsets,
+    int32_t* __restrict__ row_to_tk, int32_t* __restrict__ tk_to_row) {
+  __shared__ std::conditional_t<TABLE, RouteLds, TotalsLds> lds;
+  const int lane = lane_id();
+  const int64_t group = (int64_t)blockIdx.x * kRouteTokens * rounds;   // the workgroup's first token
+  int64_t t = group + (threadIdx.x >> 6);
+  const int n = (int)(T * k);
+  RouteTable table;
+  if constexpr (TABLE) {
+    table.c0 = (int)(group * k) >> chunk_log;
+    table.load(cnt, nchunks * E);
+  }
+  int i = (int)(min(t, T - 1) * k) + lane;
+  int e = ids[min(i, n - 1)], r = rank[min(i, n - 1)];
+  Row held;
+  if (rows) held.load(x + min(t, T - 1) * words, words);
+  if constexpr (TABLE) table.scan(lds, nchunks, E, offsets);
+  else scan_totals(total, E, lds.first, lds.wsum, offsets);
+  for (int u = 0; u < rounds && t < T; ++u) {
+    int row = -1;
+    if (lane < k) {
+      if (r >= 0) {                                // a rank marks a valid expert id
+        if constexpr (TABLE) row = lds.first[(i >> chunk_log) - table.c0][e] + r;
+        else row = lds.first[e] + cnt[(int64_t)(i >> chunk_log) * E + e] + r;
+      }
+      tk_to_row[i] = row;
+      if (row >= 0) row_to_tk[row] = i;
+    }
+    const int64_t next = t + kRouteTokens;
+    const uint4* src = x + t * words;
+    Row ahead = held;
+    i = (int)(min(next, T - 1) * k) + lane;
+    if (u + 1 < rounds) {
+      e = ids[min(i, n - 1)];
+      r = rank[min(i, n - 1)];
+      if (rows) ahead.load(x + min(next, T - 1) * words, words);
+    }
+    if (rows) copy_to_rows(held, src, words, k, row, rows);
+    held = ahead;
+    t = next;
+  }
 }
 
 // Short routing lists in one launch: every workgroup reads the whole list, counts each expert's entries and
@@ -290,6 +354,18 @@ __global__ __launch_bounds__(kWaves * 64) void combine_backward_kernel(
   }
 }
 
+constexpr int kChunkLog = kPlanChunkLogMin;
+
+// Tokens a wavefront of the main pass takes: few enough workgroups that the table scans do not add up, a
+// workgroup's entries in two chunks at most.
+#ifndef WGS
+#define WGS 1024
+#endif
+inline int rounds_of(int64_t T, int k) {
+  const int most = (1 << kChunkLog) / (kRouteTokens * k);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, T / (kRouteTokens * WGS)));
+}
+
 inline bool type_ok(int32_t t) { return t == NVFP4_IN_BF16 || t == NVFP4_IN_F32; }
 
 inline int check(int64_t T, int32_t k, int64_t H) {
@@ -305,7 +381,12 @@ using namespace nvfp4moe;
 extern "C" {
 
 NVFP4MOE_API size_t moe_permute_workspace_size(int64_t T, int32_t k, int32_t E) {
-  return T > 0 && T * (int64_t)k <= mp::kShort ? 0 : nvfp4moe_permute_workspace_size(T, k, E);
+  if (T < 0 || k < 1 || k > NVFP4MOE_MAX_TOPK || E < 1 || E > NVFP4MOE_MAX_EXPERTS || T > MOE_MAX_ROWS) return 0;
+  const int64_t n = T * (int64_t)k;
+  if (T > 0 && n <= mp::kShort) return 0;
+  // the (chunk, expert) count table, the experts' totals and a rank per entry
+  const size_t bytes = ((size_t)plan_chunks(n, mp::kChunkLog) * E + E + (size_t)n) * sizeof(int32_t);
+  return (bytes + 255) & ~(size_t)255;
 }
 
 NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t H, const int32_t* topk_ids, int32_t k,
@@ -333,19 +414,25 @@ NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t 
         src, (int)T, words, topk_ids, k, E, per, dst, expert_offsets, row_to_tk, tk_to_row, dev_err);
     return launch_status();
   }
-  const int chunk_log = plan_chunk_log(n, E), chunks = plan_chunks(n, chunk_log);
+  const int chunks = plan_chunks(n, mp::kChunkLog);
   int32_t* table = static_cast<int32_t*>(workspace);        // [chunks][E]
-  int32_t* rank = table + (int64_t)chunks * E;              // [n]
-  route_rank_kernel<<<chunks, kPlanThreads, 0, s>>>(topk_ids, (int)n, E, chunk_log, table, rank, dev_err);
-  if (T > 0 && (int64_t)chunks * E <= kCountTable) {
-    mp::permute_kernel<<<(unsigned)((T + kRouteTokens - 1) / kRouteTokens), kRouteThreads, 0, s>>>(
-        src, T, words, topk_ids, k, E, table, rank, chunks, chunk_log, dst, expert_offsets, row_to_tk, tk_to_row);
+  int32_t* total = table + (int64_t)chunks * E;             // [E]
+  int32_t* rank = total + E;                                // [n]
+  route_rank_kernel<<<chunks, kPlanThreads, 0, s>>>(topk_ids, (int)n, E, mp::kChunkLog, table, rank, dev_err);
+  if (T == 0) {
+    route_scan_kernel<<<1, kPlanThreads, 0, s>>>(table, chunks, E, expert_offsets);
     return launch_status();
   }
-  route_scan_kernel<<<1, kPlanThreads, 0, s>>>(table, chunks, E, expert_offsets);
-  if (T > 0)
-    mp::permute_rows_kernel<<<(unsigned)((T + mp::kWaves - 1) / mp::kWaves), mp::kWaves * 64, 0, s>>>(
-        src, T, words, topk_ids, k, E, table, rank, chunk_log, dst, row_to_tk, tk_to_row);
+  const int rounds = mp::rounds_of(T, k);
+  const unsigned grid = (unsigned)((T + kRouteTokens * rounds - 1) / (kRouteTokens * rounds));
+  if ((int64_t)chunks * E <= kCountTable) {
+    mp::permute_kernel<true><<<grid, kRouteThreads, 0, s>>>(src, T, words, topk_ids, k, E, table, rank, nullptr, chunks,
+        mp::kChunkLog, rounds, dst, expert_offsets, row_to_tk, tk_to_row);
+  } else {
+    mp::route_columns_kernel<<<(E + kWave - 1) / kWave, mp::kColumnWaves * 64, 0, s>>>(table, chunks, E, total);
+    mp::permute_kernel<false><<<grid, kRouteThreads, 0, s>>>(src, T, words, topk_ids, k, E, table, rank, total, chunks,
+        mp::kChunkLog, rounds, dst, expert_offsets, row_to_tk, tk_to_row);
+  }
   return launch_status();
 }
 
