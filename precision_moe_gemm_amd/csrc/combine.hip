@@ -138,22 +138,24 @@ __global__ __launch_bounds__(256) void permute_gather_kernel(
 
 // Gradient of h = w * silu(g) * u in float64 (sigmoid_f64, within 2^-50 of the
 // sigmoid; silu = g * sigmoid), each output rounded once to bf16.  DW: also w's, the sum over the row of
-// dh * silu(g) * u in float64, rounded once to float32.  The wavefront of row r then also looks at entry r
-// and writes 0 for one that has no row, so that every entry of dw is written without a fill before.
+// dh * silu(g) * u in float64, rounded once to float32.  Row r's first lane then also looks at entry r
+// and writes 0 for one that has no row, so that every entry of dw is written without a fill before.  2^lg
+// lanes take a row, fewer than a wavefront's where the row has fewer than 256 elements.
 // STREAM, where the operands do not fit the last-level cache: loads and stores are non-temporal (32768 rows of
 // 768, 403 MB: 77 us for 82; with the BF16 products that read dgu next the loads alone give 364 us for 371,
 // 643 for 686 at twice the rows, and the stores nothing more or less: 886 for 887, 1408 for 1405; at 4096
 // rows, which the caches hold, 232 for 229).
 template <bool DW, bool STREAM>
 __global__ __launch_bounds__(256) void swiglu_backward_kernel(
-    const float* __restrict__ gu, const float* __restrict__ dh, int64_t R_cap, int I,
+    const float* __restrict__ gu, const float* __restrict__ dh, int64_t R_cap, int I, int lg,
     const int32_t* __restrict__ offsets, int E, const float* __restrict__ topk_w,
     const int32_t* __restrict__ row_to_tk, uint16_t* __restrict__ dgu, const int32_t* __restrict__ tk_to_row,
     float* __restrict__ dw) {
   __shared__ double exp2_tab[64];
   stage_exp2_table(exp2_tab);
-  const int64_t r = (int64_t)blockIdx.x * kRows + (threadIdx.x >> 6);
-  if (DW && r < R_cap && lane_id() == 0) {
+  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lg;
+  const int lane = threadIdx.x & ((1 << lg) - 1);
+  if (DW && r < R_cap && lane == 0) {
     const int32_t at = tk_to_row[r];
     if (at < 0 || at >= R_cap || at >= offsets[E]) dw[r] = 0.0f;
   }
@@ -170,7 +172,7 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(
   uint16_t* orow = dgu + r * (int64_t)(2 * I);
   // 4 elements per lane per step (256 per wavefront), so that a row of any
   // multiple of 256 keeps every lane busy in the float64 work
-  for (int base = lane_id() * 4; base < I; base += kWave * 4) {
+  for (int base = lane * 4; base < I; base += 4 << lg) {
     float gs[4], us[4], ds[4];
     *reinterpret_cast<uint4*>(gs) = load16<STREAM>(grow + base);
     *reinterpret_cast<uint4*>(us) = load16<STREAM>(grow + I + base);
@@ -199,8 +201,8 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(
     store8bytes<STREAM>(orow + I + base, make_uint2(ou[0], ou[1]));
   }
   if (DW) {
-    sum = wave_sum(sum);
-    if (lane_id() == 0 && entry >= 0 && entry < R_cap) dw[entry] = (float)sum;
+    for (int off = 1 << lg >> 1; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+    if (lane == 0 && entry >= 0 && entry < R_cap) dw[entry] = (float)sum;
   }
 }
 
@@ -208,11 +210,17 @@ template <bool DW>
 void launch_swiglu_backward(const float* gu, const float* dh, int64_t R_cap, int64_t I, const int32_t* offsets, int E,
                             const float* topk_w, const int32_t* row_to_tk, uint16_t* dgu, const int32_t* tk_to_row,
                             float* dw, hipStream_t s) {
-  const unsigned grid = (unsigned)((R_cap + kRows - 1) / kRows);
+  // the least power of two of lanes that holds the row 4 elements a lane, at most a wavefront (131072 rows of
+  // 16: 11 us, of 64: 29, with a wavefront a row 92 and 93; narrower groups that go over a longer row more
+  // often take longer, 97 us for 65 at 32768 rows of 520)
+  int lg = 0;
+  while (lg < 6 && (4 << lg) < I) ++lg;
+  const int rows = 256 >> lg;
+  const unsigned grid = (unsigned)((R_cap + rows - 1) / rows);
   if (R_cap >= kLastLevelCache / (16 * I))
-    swiglu_backward_kernel<DW, true><<<grid, 256, 0, s>>>(gu, dh, R_cap, (int)I, offsets, E, topk_w, row_to_tk, dgu, tk_to_row, dw);
+    swiglu_backward_kernel<DW, true><<<grid, 256, 0, s>>>(gu, dh, R_cap, (int)I, lg, offsets, E, topk_w, row_to_tk, dgu, tk_to_row, dw);
   else
-    swiglu_backward_kernel<DW, false><<<grid, 256, 0, s>>>(gu, dh, R_cap, (int)I, offsets, E, topk_w, row_to_tk, dgu, tk_to_row, dw);
+    swiglu_backward_kernel<DW, false><<<grid, 256, 0, s>>>(gu, dh, R_cap, (int)I, lg, offsets, E, topk_w, row_to_tk, dgu, tk_to_row, dw);
 }
 
 // out[b][j][i] = in[b][i][j] for a batch of bf16 matrices: 64 x 64 tiles

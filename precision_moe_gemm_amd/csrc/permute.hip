@@ -11,8 +11,7 @@
 namespace nvfp4moe {
 namespace mp {
 
-constexpr int kWaves = 4;       // wavefronts per 256-thread workgroup
-constexpr int kCols = 512;      // elements of a row that a wavefront takes at a time, 8 a lane
+constexpr int kThreads = 256;
 
 // Rows go out with non-temporal stores: 4096 tokens x 8 rows of 4 KB take 27 us so and 36 with ordinary
 // ones (in both cases after other work has left the caches full of lines to write back).  The grouped
@@ -30,6 +29,10 @@ struct Row {
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) held[u] = src[min(u * kWave + lane_id(), words - 1)];
   }
+  __device__ __forceinline__ void load(const uint4* __restrict__ src, int words, int group) {
+    if (group < kWave) held[0] = src[min(lane_id() & (group - 1), words - 1)];
+    else load(src, words);
+  }
   __device__ __forceinline__ void copy_held(uint4* __restrict__ dst, int words) const {
 #pragma unroll
     for (int u = 0; u < kHeld; ++u)
@@ -37,9 +40,19 @@ struct Row {
   }
 };
 
-// The token's row to its k routed rows (row: lane s holds entry s's, -1 for none).
-__device__ __forceinline__ void copy_to_rows(const Row& held, const uint4* __restrict__ src, int words, int k, int row,
-                                             uint4* __restrict__ rows) {
+// The token's row to its k routed rows (row: lane s holds entry s's, -1 for none).  Rows of at most 32 words
+// (held repeated over the wavefront) go out several at a time.
+__device__ __forceinline__ void copy_to_rows(const Row& held, const uint4* __restrict__ src, int words, int group, int k,
+                                             int row, uint4* __restrict__ rows) {
+  if (group < kWave) {
+    const int c = lane_id() & (group - 1);
+    for (int s0 = 0; s0 < k; s0 += kWave / group) {
+      const int s = s0 + lane_id() / group;        // < 96
+      const int r = __shfl(row, s & (kWave - 1), kWave);
+      if (s < k && r >= 0 && c < words) store_row(rows + (int64_t)r * words + c, held.held[0]);
+    }
+    return;
+  }
   for (int s = 0; s < k; ++s) {
     const int r = __shfl(row, s, kWave);
     if (r >= 0) held.copy_held(rows + (int64_t)r * words, words);
@@ -126,22 +139,22 @@ template <bool TABLE>
 __global__ __launch_bounds__(kRouteThreads) void permute_kernel(
     const uint4* __restrict__ x, int64_t T, int words, const int32_t* __restrict__ ids, int k, int E,
     const int32_t* __restrict__ cnt, const int32_t* __restrict__ rank, const int32_t* __restrict__ total, int nchunks,
-    int chunk_log, int rounds, uint4* __restrict__ rows, int32_t* __restrict__ offsets,
+    int chunk_log, int rounds, int group, uint4* __restrict__ rows, int32_t* __restrict__ offsets,
     int32_t* __restrict__ row_to_tk, int32_t* __restrict__ tk_to_row) {
   __shared__ std::conditional_t<TABLE, RouteLds, TotalsLds> lds;
   const int lane = lane_id();
-  const int64_t group = (int64_t)blockIdx.x * kRouteTokens * rounds;   // the workgroup's first token
-  int64_t t = group + (threadIdx.x >> 6);
+  const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens * rounds;   // the workgroup's first token
+  int64_t t = t0 + (threadIdx.x >> 6);
   const int n = (int)(T * k);
   RouteTable table;
   if constexpr (TABLE) {
-    table.c0 = (int)(group * k) >> chunk_log;
+    table.c0 = (int)(t0 * k) >> chunk_log;
     table.load(cnt, nchunks * E);
   }
   int i = (int)(min(t, T - 1) * k) + lane;
   int e = ids[min(i, n - 1)], r = rank[min(i, n - 1)];
   Row held;
-  if (rows) held.load(x + min(t, T - 1) * words, words);
+  if (rows) held.load(x + min(t, T - 1) * words, words, group);
   if constexpr (TABLE) table.scan(lds, nchunks, E, offsets);
   else scan_totals(total, E, lds.first, lds.wsum, offsets);
   for (int u = 0; u < rounds && t < T; ++u) {
@@ -161,9 +174,9 @@ __global__ __launch_bounds__(kRouteThreads) void permute_kernel(
     if (u + 1 < rounds) {
       e = ids[min(i, n - 1)];
       r = rank[min(i, n - 1)];
-      if (rows) ahead.load(x + min(next, T - 1) * words, words);
+      if (rows) ahead.load(x + min(next, T - 1) * words, words, group);
     }
-    if (rows) copy_to_rows(held, src, words, k, row, rows);
+    if (rows) copy_to_rows(held, src, words, group, k, row, rows);
     held = ahead;
     t = next;
   }
@@ -253,85 +266,94 @@ __global__ __launch_bounds__(kRouteThreads) void permute_short_kernel(
   }
 }
 
-// One wavefront per 512 columns of a token's sum, taken in FP32 and in slot order with products and sums
-// rounded apart; the loads of 8 slots are issued before the first is added.  They are non-temporal: each row
-// is read once (4096 tokens x 8 rows of 2048 bf16: 27 us for 29; 151 MB, so 5.6 TB/s).
+// Short rows leave most of a wavefront without columns, so a group of lanes takes an item (a token, a routed
+// entry): the least power of two that holds the row 8 elements a lane, at most a wavefront (16384 tokens x 8
+// rows of 64 bf16: the combine 5.0 us and its gradient 7.9, with a wavefront an item 14.3 and 44.8).
+inline int log_lanes_for(int64_t words) {
+  int lg = 0;
+  while (lg < 6 && (1 << lg) < words) ++lg;
+  return lg;
+}
+
+// One group of 2^lg lanes per 8 * 2^lg columns of a token's sum, taken in FP32 and in slot order with products
+// and sums rounded apart; the loads of 8 slots are issued before the first is added.  They are non-temporal:
+// each row is read once (4096 tokens x 8 rows of 2048 bf16: 27 us for 29; 151 MB, so 5.6 TB/s).  Every lane
+// reads the token's rows and weights itself (handed round a wavefront with shuffles they take 26.2 us for 26.5
+// there, 36.9 for 34.4 at 16384 tokens with 2 rows).
 template <bool DF32, bool YF32>
-__global__ __launch_bounds__(kWaves * 64) void combine_kernel(
-    const void* __restrict__ d, int64_t T, int k, int H, const int32_t* __restrict__ tk_to_row,
+__global__ __launch_bounds__(kThreads) void combine_kernel(
+    const void* __restrict__ d, int T, int k, int H, int lg, const int32_t* __restrict__ tk_to_row,
     const float* __restrict__ topk_w, void* __restrict__ y) {
-  const int pieces = (H + kCols - 1) / kCols;
-  const int64_t item = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  const int64_t t = item / pieces;
-  if (t >= T) return;
-  const int lane = lane_id();
-  const int my_row = lane < k ? tk_to_row[t * k + lane] : -1;
-  const float my_w = (lane < k && topk_w) ? topk_w[t * k + lane] : 1.0f;
-  const int c = (int)(item - t * pieces) * kCols + 8 * lane;
-  const bool inside = c < H;
+  const uint32_t pieces = (uint32_t)(H + (8 << lg) - 1) >> (lg + 3);
+  const uint32_t item = (blockIdx.x * kThreads + threadIdx.x) >> lg, t = item / pieces;
+  if (t >= (uint32_t)T) return;
+  const int lane = threadIdx.x & ((1 << lg) - 1);
+  const int c = (int)(((item - t * pieces) << lg) + lane) * 8, R = T * k;
+  if (c >= H) return;
+  const int32_t* map = tk_to_row + (int64_t)t * k;
+  const float* wt = topk_w ? topk_w + (int64_t)t * k : nullptr;
   float acc[8] = {};
   bool started = false;
   for (int s0 = 0; s0 < k; s0 += 8) {
     Raw8<DF32> raw[8];
-    bool ok[8];
+    int row[8];
     float ws[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int row = __shfl(my_row, s0 + u, kWave);   // s0 + u < 40: a lane; entries past k have no row
-      ws[u] = __shfl(my_w, s0 + u, kWave);
-      ok[u] = row >= 0 && row < T * k && inside;
-      if (ok[u]) raw[u] = load8<DF32, true>(d, (int64_t)row * H + c);
+      row[u] = s0 + u < k ? map[s0 + u] : -1;
+      ws[u] = wt && s0 + u < k ? wt[s0 + u] : 1.0f;
+      if (row[u] >= R) row[u] = -1;
     }
 #pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (row[u] >= 0) raw[u] = load8<DF32, true>(d, (int64_t)row[u] * H + c);
+#pragma unroll
     for (int u = 0; u < 8; ++u) {
-      if (!ok[u]) continue;
+      if (row[u] < 0) continue;
       float v[8];
       unpack8<DF32>(raw[u], v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float x = topk_w ? ws[u] * v[j] : v[j];
+        const float x = wt ? ws[u] * v[j] : v[j];
         acc[j] = started ? acc[j] + x : x;
       }
       started = true;
     }
   }
-  if (inside) store8<YF32>(y, t * H + c, acc);
+  store8<YF32>(y, (int64_t)t * H + c, acc);
 }
 
-// One wavefront per entry i = (t, s): dd[row] = w_i dy[t], dw_i = <dy[t], d[row]> in FP32, added within
-// the lane and then over the wavefront in a fixed order.  An entry without a row has dw_i = 0.  The loads of
-// kAhead pieces of 512 columns are issued before the first is used (4096 tokens x 8 rows of 2048 bf16: 58 us
-// with 4, 65 with 2, 70 with 1); the token's k wavefronts share dy[t] in the caches.  STREAM, where the
-// operands do not fit the last-level cache: d and dd are non-temporal (54 us for 58; 285 MB, so 5.3 TB/s;
-// with the BF16 input-gradient product that reads dd next 256 us for 263, 377 for 390 at 8192 tokens, but 206
-// for 203 at 2048 and 166 for 162 at 512, where the caches hold them).
-constexpr int kAhead = 4;
-template <bool YF32, bool DF32, bool STREAM>
-__global__ __launch_bounds__(kWaves * 64) void combine_backward_kernel(
-    const void* __restrict__ dy, const void* __restrict__ d, int64_t R, int k, int H,
+// One group of 2^lg lanes per entry i = (t, s): dd[row] = w_i dy[t], dw_i = <dy[t], d[row]> in FP32, added within
+// the lane and then over the group in a fixed order.  An entry without a row has dw_i = 0.  The loads of AHEAD
+// pieces of 8 * 2^lg columns are issued before the first is used (4096 tokens x 8 rows of 2048 bf16: 58 us
+// with 4, 65 with 2, 70 with 1); a token's entries share dy[t] in the caches.  STREAM, where the operands do
+// not fit the last-level cache: d and dd are non-temporal (54 us for 58; 285 MB, so 5.3 TB/s; with the BF16
+// input-gradient product that reads dd next 256 us for 263, 377 for 390 at 8192 tokens, but 206 for 203 at
+// 2048 and 166 for 162 at 512, where the caches hold them).
+template <bool YF32, bool DF32, bool STREAM, int AHEAD>
+__global__ __launch_bounds__(kThreads) void combine_backward_kernel(
+    const void* __restrict__ dy, const void* __restrict__ d, int R, int k, int H, int lg,
     const int32_t* __restrict__ tk_to_row, const float* __restrict__ topk_w, void* __restrict__ dd,
     float* __restrict__ dw) {
-  const int64_t i = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (i >= R) return;
-  const int64_t row = tk_to_row[i];
-  const bool has = row >= 0 && row < R;
-  const int64_t t = i / k;
-  const int lane = lane_id();
+  const int i = (int)((blockIdx.x * kThreads + threadIdx.x) >> lg);
+  const int lane = threadIdx.x & ((1 << lg) - 1), step = 8 << lg;
+  const int64_t row = i < R ? tk_to_row[i] : -1;
   float sum = 0.0f;
-  if (has) {
+  if (row >= 0 && row < R) {
+    const int64_t t = (uint32_t)i / (uint32_t)k;
     const float w = topk_w ? topk_w[i] : 1.0f;
-    for (int c0 = 8 * lane; c0 < H; c0 += kAhead * kCols) {
-      Raw8<YF32> yr[kAhead];
-      Raw8<DF32> dr[kAhead];
+    for (int c0 = 8 * lane; c0 < H; c0 += AHEAD * step) {
+      Raw8<YF32> yr[AHEAD];
+      Raw8<DF32> dr[AHEAD];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int c = min(c0 + u * kCols, H - 8);
+      for (int u = 0; u < AHEAD; ++u) {
+        const int c = min(c0 + u * step, H - 8);
         yr[u] = load8<YF32>(dy, t * H + c);
         if (dw) dr[u] = load8<DF32, STREAM>(d, row * H + c);
       }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int c = c0 + u * kCols;
+      for (int u = 0; u < AHEAD; ++u) {
+        const int c = c0 + u * step;
         if (c >= H) continue;
         float y[8], v[8];
         unpack8<YF32>(yr[u], y);
@@ -349,8 +371,8 @@ __global__ __launch_bounds__(kWaves * 64) void combine_backward_kernel(
     }
   }
   if (dw) {
-    sum = wave_sum(sum);
-    if (lane == 0) dw[i] = sum;
+    for (int off = 1 << lg >> 1; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+    if (lane == 0 && i < R) dw[i] = sum;
   }
 }
 
@@ -358,12 +380,10 @@ constexpr int kChunkLog = kPlanChunkLogMin;
 
 // Tokens a wavefront of the main pass takes: few enough workgroups that the table scans do not add up, a
 // workgroup's entries in two chunks at most.
-#ifndef WGS
-#define WGS 1024
-#endif
+constexpr int kMainGroups = 1024;
 inline int rounds_of(int64_t T, int k) {
   const int most = (1 << kChunkLog) / (kRouteTokens * k);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(most, T / (kRouteTokens * WGS)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, T / (kRouteTokens * kMainGroups)));
 }
 
 inline bool type_ok(int32_t t) { return t == NVFP4_IN_BF16 || t == NVFP4_IN_F32; }
@@ -427,11 +447,11 @@ NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t 
   const unsigned grid = (unsigned)((T + kRouteTokens * rounds - 1) / (kRouteTokens * rounds));
   if ((int64_t)chunks * E <= kCountTable) {
     mp::permute_kernel<true><<<grid, kRouteThreads, 0, s>>>(src, T, words, topk_ids, k, E, table, rank, nullptr, chunks,
-        mp::kChunkLog, rounds, dst, expert_offsets, row_to_tk, tk_to_row);
+        mp::kChunkLog, rounds, 1 << mp::log_lanes_for(words), dst, expert_offsets, row_to_tk, tk_to_row);
   } else {
     mp::route_columns_kernel<<<(E + kWave - 1) / kWave, mp::kColumnWaves * 64, 0, s>>>(table, chunks, E, total);
     mp::permute_kernel<false><<<grid, kRouteThreads, 0, s>>>(src, T, words, topk_ids, k, E, table, rank, total, chunks,
-        mp::kChunkLog, rounds, dst, expert_offsets, row_to_tk, tk_to_row);
+        mp::kChunkLog, rounds, 1 << mp::log_lanes_for(words), dst, expert_offsets, row_to_tk, tk_to_row);
   }
   return launch_status();
 }
@@ -440,16 +460,17 @@ NVFP4MOE_API int moe_combine(const void* d, int32_t d_dtype, int64_t T, int32_t 
                              const float* topk_w, void* y, int32_t y_dtype, void* stream) {
   if (!mp::type_ok(d_dtype) || !mp::type_ok(y_dtype)) return NVFP4_ERR_ARG;
   if (const int bad = mp::check(T, k, H)) return bad;
-  const int64_t items = T * ((H + mp::kCols - 1) / mp::kCols);
-  if (items > MOE_MAX_ROWS) return NVFP4_ERR_SHAPE;
+  if (T * ((H + 511) / 512) > MOE_MAX_ROWS) return NVFP4_ERR_SHAPE;
   if (T == 0) return NVFP4_OK;
   if (!d || !tk_to_row || !y) return NVFP4_ERR_NULL;
   if (!aligned16(d) || !aligned16(tk_to_row) || !aligned16(topk_w) || !aligned16(y)) return NVFP4_ERR_ALIGN;
   if (d == y) return NVFP4_ERR_ARG;
-  const int64_t grid = (items + mp::kWaves - 1) / mp::kWaves;
+  const int lg = mp::log_lanes_for(H / 8), per = mp::kThreads >> lg;
+  const int64_t items = T * ((H + (8 << lg) - 1) >> (lg + 3));
+  const unsigned grid = (unsigned)((items + per - 1) / per);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool df = d_dtype == NVFP4_IN_F32, yf = y_dtype == NVFP4_IN_F32;
-#define MP_COMBINE(D, Y) mp::combine_kernel<D, Y><<<(unsigned)grid, mp::kWaves * 64, 0, s>>>(d, T, k, (int)H, tk_to_row, topk_w, y)
+#define MP_COMBINE(D, Y) mp::combine_kernel<D, Y><<<grid, mp::kThreads, 0, s>>>(d, (int)T, k, (int)H, lg, tk_to_row, topk_w, y)
   if (df) yf ? MP_COMBINE(true, true) : MP_COMBINE(true, false);
   else yf ? MP_COMBINE(false, true) : MP_COMBINE(false, false);
 #undef MP_COMBINE
@@ -469,15 +490,21 @@ NVFP4MOE_API int moe_combine_backward(const void* dy, int32_t dy_dtype, const vo
   if (dd && (dd == d || dd == dy)) return NVFP4_ERR_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t R = T * (int64_t)k;
-  const unsigned grid = (unsigned)((R + mp::kWaves - 1) / mp::kWaves);
+  const int lg = mp::log_lanes_for(H / 8), per = mp::kThreads >> lg;
+  const unsigned grid = (unsigned)((R + per - 1) / per);
   const bool yf = dy_dtype == NVFP4_IN_F32, df = d_dtype == NVFP4_IN_F32;
   const int64_t bytes = T * H * (yf ? 4 : 2) + R * H * (df ? 4 : 2) * ((dtopk_w ? 1 : 0) + (dd ? 1 : 0));
-  const bool stream_out = bytes >= kLastLevelCache;
-#define MP_BACKWARD(Y, D, S) \
-  mp::combine_backward_kernel<Y, D, S><<<grid, mp::kWaves * 64, 0, s>>>(dy, d, R, k, (int)H, tk_to_row, topk_w, dd, dtopk_w)
-#define MP_BACKWARD_BY(Y, D) (stream_out ? MP_BACKWARD(Y, D, true) : MP_BACKWARD(Y, D, false))
-  if (yf) df ? MP_BACKWARD_BY(true, true) : MP_BACKWARD_BY(true, false);
-  else df ? MP_BACKWARD_BY(false, true) : MP_BACKWARD_BY(false, false);
+  const bool streamed = bytes >= kLastLevelCache;
+#define MP_BACKWARD(Y, D, S, A)                                                                                  \
+  mp::combine_backward_kernel<Y, D, S, A><<<grid, mp::kThreads, 0, s>>>(dy, d, (int)R, k, (int)H, lg, tk_to_row, \
+                                                                        topk_w, dd, dtopk_w)
+#define MP_BACKWARD_BY(Y, D)                                                                            \
+  do {                                                                                                  \
+    if (H <= 512) streamed ? MP_BACKWARD(Y, D, true, 1) : MP_BACKWARD(Y, D, false, 1);                  \
+    else streamed ? MP_BACKWARD(Y, D, true, 4) : MP_BACKWARD(Y, D, false, 4);                           \
+  } while (0)
+  if (yf) { if (df) MP_BACKWARD_BY(true, true); else MP_BACKWARD_BY(true, false); }
+  else { if (df) MP_BACKWARD_BY(false, true); else MP_BACKWARD_BY(false, false); }
 #undef MP_BACKWARD_BY
 #undef MP_BACKWARD
   return launch_status();
