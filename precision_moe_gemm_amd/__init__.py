@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from array import array
 
 import torch
 
@@ -609,11 +610,14 @@ def _call(name, dev, *args):
 
 def _arg(t, name, dtypes, dev, ndim=None, numel=None):
     """_req of a tensor that must be there, and that it lies on device `dev`."""
+    # one test that all is well (small calls are bound by the host), then the ones that say what is not
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev and t.is_contiguous()
+            and (ndim is None or t.dim() == ndim) and (numel is None or t.numel() >= numel) and dev >= 0):
+        return
     if t is None:
         raise TypeError(f"{name} must be a torch.Tensor")
     _req(t, name, dtypes, ndim, numel)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
 def _head(t, name, dtypes, ndim):
@@ -935,22 +939,19 @@ _GRAD_TYPES = {torch.float32: 1, **dict.fromkeys(_BF16, 0)}
 
 
 def _grads(grads, what, dev):
-    """The tensors' (pointers, types, sizes) as C arrays, and their device."""
-    n = len(grads)
+    """The tensors' addresses, types and sizes as C arrays (to be kept during the call), and their device."""
     # models hold hundreds of tensors, so the checks run over the whole list; the loop names the one that fails
-    if n and all(isinstance(t, torch.Tensor) for t in grads):
+    if grads and all(isinstance(t, torch.Tensor) for t in grads):
         where = set(map(torch.Tensor.get_device, grads))
         types = [_GRAD_TYPES.get(t.dtype, -1) for t in grads]
-        if len(where) == 1 and -1 not in types and all(map(torch.Tensor.is_contiguous, grads)):
-            at = where.pop()
-            if at >= 0 and dev in (None, at):
-                return ((_P * n)(*map(torch.Tensor.data_ptr, grads)), (_I32 * n)(*types),
-                        (_I64 * n)(*map(torch.Tensor.numel, grads)), at)
+        at = where.pop()
+        if not where and at >= 0 and dev in (None, at) and -1 not in types and all(map(torch.Tensor.is_contiguous, grads)):
+            return array("Q", map(torch.Tensor.data_ptr, grads)), array("i", types), array("q", map(torch.Tensor.numel, grads)), at
     for j, t in enumerate(grads):
         if dev is None:
             dev = _head(t, f"{what}[0]", _BF16_F32, None)
         _arg(t, f"{what}[{j}]", _BF16_F32, dev)
-    return (_P * 0)(), (_I32 * 0)(), (_I64 * 0)(), dev
+    return array("Q"), array("i"), array("q"), dev
 
 
 def _grad_buffers(n, norm, workspace, dev):
@@ -973,7 +974,8 @@ def grad_norm(grads, norm=None, workspace=None):
     ptrs, types, sizes, dev = _grads(grads, "grads", None if norm is None else norm.get_device())
     dev = torch.cuda.current_device() if dev is None else dev
     norm, workspace = _grad_buffers(len(grads), norm, workspace, dev)
-    _call("moe_grad_norm", dev, ptrs, types, sizes, len(grads), norm.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _call("moe_grad_norm", dev, *(a.buffer_info()[0] for a in (ptrs, types, sizes)), len(grads), norm.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return norm
 
 
@@ -987,11 +989,11 @@ def grad_clip(grads, max_norm: float, out=None, norm=None, workspace=None):
     if len(out) != len(grads):
         raise ValueError(f"{len(out)} outputs for {len(grads)} tensors")
     outs, otypes, osizes, _ = _grads(out, "out", dev)
-    if bytes(otypes) != bytes(types) or bytes(osizes) != bytes(sizes):
+    if otypes != types or osizes != sizes:
         raise ValueError("out must have the sizes and types of grads")
     norm, workspace = _grad_buffers(len(grads), norm, workspace, dev)
-    _call("moe_grad_clip", dev, ptrs, outs, types, sizes, len(grads), max_norm, norm.data_ptr(), workspace.data_ptr(),
-          workspace.numel())
+    _call("moe_grad_clip", dev, *(a.buffer_info()[0] for a in (ptrs, outs, types, sizes)), len(grads), max_norm,
+          norm.data_ptr(), workspace.data_ptr(), workspace.numel())
     return norm, out
 
 

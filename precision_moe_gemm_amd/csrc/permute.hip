@@ -95,8 +95,8 @@ __global__ __launch_bounds__(kColumnWaves * 64) void route_columns_kernel(int32_
 }
 
 // The expert offsets from the experts' totals, into LDS (and memory, from workgroup 0).
-__device__ __forceinline__ void scan_totals(const int32_t* __restrict__ total, int E, int32_t* __restrict__ first,
-                                            int32_t* __restrict__ wsum, int32_t* __restrict__ offsets) {
+__device__ __forceinline__ void scan_totals(const int32_t* total, int E, int32_t* first, int32_t* wsum,
+                                            int32_t* __restrict__ offsets) {
   const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
   int tot[kRouteExp], sum = 0;
 #pragma unroll
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(kRouteThreads) void permute_kernel(
 }
 
 // Short routing lists in one launch: every workgroup reads the whole list, counts each expert's entries and
-// those before its own (LDS), scans the counts, and ranks the entries of its own `per` tokens; its
+// those before its own (LDS; sums of whole numbers, whose order changes nothing), scans the counts, and ranks the entries of its own `per` tokens; its
 // wavefronts then take one (token, slot) row each.
 constexpr int kShort = 6144;            // entries; 128 experts, in one launch and in two: 3072 entries 7.5 us
                                         // for 9.8, 6144 10.0 for 10.8, 8192 12.2 for 12.2, 16384 21.9 for 19.2
@@ -192,12 +192,12 @@ __global__ __launch_bounds__(kRouteThreads) void permute_short_kernel(
     const uint4* __restrict__ x, int T, int words, const int32_t* __restrict__ ids, int k, int E, int per,
     uint4* __restrict__ rows, int32_t* __restrict__ offsets, int32_t* __restrict__ row_to_tk,
     int32_t* __restrict__ tk_to_row, int32_t* __restrict__ dev_err) {
-  __shared__ int32_t total[NVFP4MOE_MAX_EXPERTS], first[NVFP4MOE_MAX_EXPERTS];
+  __shared__ int32_t total[NVFP4MOE_MAX_EXPERTS], before[NVFP4MOE_MAX_EXPERTS], first[NVFP4MOE_MAX_EXPERTS];
   __shared__ int32_t own_e[kShortTokens * NVFP4MOE_MAX_TOPK], own_row[kShortTokens * NVFP4MOE_MAX_TOPK];
   __shared__ int32_t wsum[kRouteWaves];
-  const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
+  const int tid = threadIdx.x, wave = tid >> 6;
   const int n = T * k, t0 = blockIdx.x * per, e0 = t0 * k, own = min(per, T - t0) * k;
-  for (int e = tid; e < E; e += kRouteThreads) total[e] = first[e] = 0;
+  for (int e = tid; e < E; e += kRouteThreads) total[e] = before[e] = 0;
   __syncthreads();
   bool bad = false;
   for (int i = tid; i < n; i += kRouteThreads) {
@@ -205,46 +205,19 @@ __global__ __launch_bounds__(kRouteThreads) void permute_short_kernel(
     const bool valid = e >= 0 && e < E;
     if (valid) {
       atomicAdd(&total[e], 1);
-      if (i < e0) atomicAdd(&first[e], 1);
+      if (i < e0) atomicAdd(&before[e], 1);
     }
     bad |= !valid;
     if (i >= e0 && i < e0 + own) own_e[i - e0] = valid ? e : -1;
   }
   if (bad && dev_err && blockIdx.x == 0) atomicOr(dev_err, NVFP4_DEVERR_BAD_EXPERT);
   __syncthreads();
-  int tot[kRouteExp], sum = 0;
-#pragma unroll
-  for (int u = 0; u < kRouteExp; ++u) {
-    const int e = kRouteExp * tid + u;
-    tot[u] = e < E ? total[e] : 0;
-    sum += tot[u];
-  }
-  int incl = sum;
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const int y = __shfl_up(incl, off, kWave);
-    if (lane >= off) incl += y;
-  }
-  if (lane == kWave - 1) wsum[wave] = incl;
-  __syncthreads();
-  int at = incl - sum;
-  for (int w = 0; w < wave; ++w) at += wsum[w];
-#pragma unroll
-  for (int u = 0; u < kRouteExp; ++u) {
-    const int e = kRouteExp * tid + u;
-    if (e < E) {
-      first[e] += at;
-      if (blockIdx.x == 0) offsets[e] = at;
-    }
-    at += tot[u];
-  }
-  if (blockIdx.x == 0 && tid == kRouteThreads - 1) offsets[E] = at;
-  __syncthreads();
+  scan_totals(total, E, first, wsum, offsets);
   if (tid < own) {
     const int e = own_e[tid];
     int row = -1;
     if (e >= 0) {
-      row = first[e];
+      row = first[e] + before[e];
       for (int j = 0; j < tid; ++j) row += own_e[j] == e;
       row_to_tk[row] = e0 + tid;
     }

@@ -80,7 +80,7 @@ def test_permute(T, E, k, H, kind, dtype):
         assert torch.equal(maps["row_to_tk"][:n], got["row_to_tk"][:n])
 
 
-@pytest.mark.parametrize("T,E,k", [(40000, 128, 8), (33000, 512, 4), (70000, 16, 1)])
+@pytest.mark.parametrize("T,E,k", [(40000, 128, 8), (33000, 512, 4), (70000, 16, 1), (20000, 1000, 31), (9000, 300, 32)])
 def test_permute_long_lists(T, E, k):
     """Routing lists of many chunks: the same maps as the quantising permutation's."""
     ids, _ = routing("uniform", T, E, k, 32, 0.01)
