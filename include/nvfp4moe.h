@@ -579,7 +579,8 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  * The router, the token sort and its way back, and their gradients: what lies between a
  * router's logits and the experts' products.  Rows and logits are bf16 bits or float, by a
  * type NVFP4_IN_BF16 or NVFP4_IN_F32; sums are taken in FP32 or FP64, and a bf16 result is
- * rounded once, to nearest even.
+ * rounded once, to nearest even.  Rows (x, d, dy, gu, ...) and workspaces start at 16-byte
+ * boundaries; logits, gradients to clip, ids, maps and weights at any of their elements.
  *
  * moe_router_topk - the k experts of each token and their weights.
  *   logits   [T][E] of dtype

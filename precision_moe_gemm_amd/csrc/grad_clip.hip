@@ -227,7 +227,7 @@ int check(const void* const* in, const int32_t* dtype, const int64_t* numel, int
     bytes += numel[i] * (dtype[i] == NVFP4_IN_F32 ? 4 : 2);
     if (bytes > MOE_MAX_GRAD_BYTES) return NVFP4_ERR_SHAPE;
     if (numel[i] && !in[i]) return NVFP4_ERR_NULL;
-    if (reinterpret_cast<uintptr_t>(in[i]) & (dtype[i] == NVFP4_IN_F32 ? 3 : 1)) return NVFP4_ERR_ALIGN;
+    if (!aligned_to(in[i], dtype[i] == NVFP4_IN_F32 ? 4 : 2)) return NVFP4_ERR_ALIGN;
   }
   return NVFP4_OK;
 }
@@ -326,7 +326,7 @@ NVFP4MOE_API int moe_grad_norm(const void* const* grads, const int32_t* dtypes, 
                                float* norm, void* workspace, size_t workspace_bytes, void* stream) {
   if (const int bad = gc::check(grads, dtypes, numel, n)) return bad;
   if (!norm || !workspace) return NVFP4_ERR_NULL;
-  if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(norm) & 3)) return NVFP4_ERR_ALIGN;
+  if (!aligned16(workspace) || !aligned_to(norm, 4)) return NVFP4_ERR_ALIGN;
   if (workspace_bytes < moe_grad_workspace_size(n)) return NVFP4_ERR_WORKSPACE;
   return gc::run(grads, nullptr, dtypes, numel, n, 0.0, norm, static_cast<double*>(workspace),
                  static_cast<hipStream_t>(stream));
@@ -339,7 +339,7 @@ NVFP4MOE_API int moe_grad_clip(const void* const* grads, void* const* out, const
   if (const int bad = gc::check(grads, dtypes, numel, n)) return bad;
   if (!norm || !workspace || (n && !out)) return NVFP4_ERR_NULL;
   if (const int bad = gc::check(out, dtypes, numel, n)) return bad;
-  if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(norm) & 3)) return NVFP4_ERR_ALIGN;
+  if (!aligned16(workspace) || !aligned_to(norm, 4)) return NVFP4_ERR_ALIGN;
   if (workspace_bytes < moe_grad_workspace_size(n)) return NVFP4_ERR_WORKSPACE;
   if (const int bad = gc::overlaps(grads, out, dtypes, numel, n)) return bad;
   return gc::run(grads, out, dtypes, numel, n, max_norm, norm, static_cast<double*>(workspace),

@@ -391,8 +391,8 @@ NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t 
   const size_t need = moe_permute_workspace_size(T, k, E);
   if (!expert_offsets || (need && !workspace)) return NVFP4_ERR_NULL;
   if (T > 0 && (!topk_ids || !row_to_tk || !tk_to_row || !x != !rows)) return NVFP4_ERR_NULL;
-  if (!aligned16(x) || !aligned16(topk_ids) || !aligned16(rows) || !aligned16(expert_offsets) ||
-      !aligned16(row_to_tk) || !aligned16(tk_to_row) || !aligned16(workspace))
+  if (!aligned16(x) || !aligned16(rows) || !aligned16(workspace) || !aligned_to(topk_ids, 4) ||
+      !aligned_to(expert_offsets, 4) || !aligned_to(row_to_tk, 4) || !aligned_to(tk_to_row, 4) || !aligned_to(dev_err, 4))
     return NVFP4_ERR_ALIGN;
   if (x && x == rows) return NVFP4_ERR_ARG;
   if (workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
@@ -436,7 +436,7 @@ NVFP4MOE_API int moe_combine(const void* d, int32_t d_dtype, int64_t T, int32_t 
   if (T * ((H + 511) / 512) > MOE_MAX_ROWS) return NVFP4_ERR_SHAPE;
   if (T == 0) return NVFP4_OK;
   if (!d || !tk_to_row || !y) return NVFP4_ERR_NULL;
-  if (!aligned16(d) || !aligned16(tk_to_row) || !aligned16(topk_w) || !aligned16(y)) return NVFP4_ERR_ALIGN;
+  if (!aligned16(d) || !aligned16(y) || !aligned_to(tk_to_row, 4) || !aligned_to(topk_w, 4)) return NVFP4_ERR_ALIGN;
   if (d == y) return NVFP4_ERR_ARG;
   const int lg = mp::log_lanes_for(H / 8), per = mp::kThreads >> lg;
   const int64_t items = T * ((H + (8 << lg) - 1) >> (lg + 3));
@@ -457,8 +457,8 @@ NVFP4MOE_API int moe_combine_backward(const void* dy, int32_t dy_dtype, const vo
   if (const int bad = mp::check(T, k, H)) return bad;
   if (T == 0) return NVFP4_OK;
   if (!dy || !tk_to_row || (!dd && !dtopk_w) || (dtopk_w && !d)) return NVFP4_ERR_NULL;
-  if (!aligned16(dy) || !aligned16(d) || !aligned16(tk_to_row) || !aligned16(topk_w) || !aligned16(dd) ||
-      !aligned16(dtopk_w))
+  if (!aligned16(dy) || !aligned16(d) || !aligned16(dd) || !aligned_to(tk_to_row, 4) || !aligned_to(topk_w, 4) ||
+      !aligned_to(dtopk_w, 4))
     return NVFP4_ERR_ALIGN;
   if (dd && (dd == d || dd == dy)) return NVFP4_ERR_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -336,7 +336,8 @@ NVFP4MOE_API int moe_router_topk(const void* logits, int32_t dtype, int64_t T, i
   if (const int bad = router::check(T, E, k, dtype, renorm)) return bad;
   if (T == 0) return NVFP4_OK;
   if (!logits || !topk_ids || !topk_w) return NVFP4_ERR_NULL;
-  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_w)) return NVFP4_ERR_ALIGN;
+  if (!aligned_to(logits, dtype == NVFP4_IN_F32 ? 4 : 2) || !aligned_to(topk_ids, 4) || !aligned_to(topk_w, 4))
+    return NVFP4_ERR_ALIGN;
   ROUTER_DISPATCH(router::topk_kernel, logits, T, (int)E, (int)k, (int)renorm, topk_ids, topk_w);
   return launch_status();
 }
@@ -347,7 +348,9 @@ NVFP4MOE_API int moe_router_topk_backward(const void* logits, int32_t dtype, con
   if (const int bad = router::check(T, E, k, dtype, renorm)) return bad;
   if (T == 0) return NVFP4_OK;
   if (!topk_ids || !topk_w || !dtopk_w || !dlogits || (!renorm && !logits)) return NVFP4_ERR_NULL;
-  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_w) || !aligned16(dtopk_w) || !aligned16(dlogits))
+  const int size = dtype == NVFP4_IN_F32 ? 4 : 2;
+  if (!aligned_to(logits, size) || !aligned_to(dlogits, size) || !aligned_to(topk_ids, 4) || !aligned_to(topk_w, 4) ||
+      !aligned_to(dtopk_w, 4))
     return NVFP4_ERR_ALIGN;
   if (dlogits == logits) return NVFP4_ERR_ARG;
   ROUTER_DISPATCH(router::topk_backward_kernel, logits, topk_ids, topk_w, dtopk_w, T, (int)E, (int)k, (int)renorm, dlogits);

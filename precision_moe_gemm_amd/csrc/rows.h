@@ -6,6 +6,8 @@
 
 namespace nvfp4moe {
 
+inline bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
 constexpr int64_t kLastLevelCache = 256ll << 20;   // bytes
 
 // 16 bytes; STREAM: non-temporal, for data that the caches would not hold until it is used again

@@ -25,13 +25,13 @@ def test_router(lib):
             assert f(**kw) == ERR_SHAPE, kw
         for n in ("ids", "w"):
             assert f(**{n: None}) == ERR_NULL, n
-            assert f(**{n: P + 4}) == ERR_ALIGN, n
-        assert f(l=P + 2) == ERR_ALIGN
+            assert f(**{n: P + 2}) == ERR_ALIGN, n
+        assert f(l=P + 1) == ERR_ALIGN and f(l=P + 2, dt=1) == ERR_ALIGN
         assert f(T=0, l=None, ids=None, w=None) == OK
     assert fwd(l=None) == ERR_NULL
     assert bwd(l=None, rn=0) == ERR_NULL
     assert bwd(dw=None) == ERR_NULL and bwd(dl=None) == ERR_NULL
-    assert bwd(dw=P + 8) == ERR_ALIGN and bwd(dl=Q + 2) == ERR_ALIGN
+    assert bwd(dw=P + 1) == ERR_ALIGN and bwd(dl=Q + 1) == ERR_ALIGN and bwd(dl=Q + 2, dt=1) == ERR_ALIGN
     assert bwd(dl=P) == ERR_ARG                                # over the logits
 
 
@@ -48,7 +48,7 @@ def test_permute(lib):
         assert f(**kw) == ERR_SHAPE, kw
     for n in ("ids", "off", "r2t", "t2r", "ws", "x", "rows"):
         assert f(**{n: None}) == ERR_NULL, n
-        assert f(**{n: P + 4}) == ERR_ALIGN, n
+        assert f(**{n: P + (8 if n in ("ws", "x", "rows") else 2)}) == ERR_ALIGN, n
     assert f(wsb=size - 1) == ERR_WORKSPACE
     assert f(x=None, rows=None, H=3, wsb=0) == ERR_WORKSPACE    # the maps alone: H unused
 
@@ -64,7 +64,7 @@ def test_combine(lib):
     for n in ("d", "map", "y"):
         assert f(**{n: None}) == ERR_NULL, n
     for n in ("d", "map", "w", "y"):
-        assert f(**{n: P + 8}) == ERR_ALIGN, n
+        assert f(**{n: P + (2 if n in ("map", "w") else 8)}) == ERR_ALIGN, n
     assert f(T=0, d=None, map=None, w=None, y=None) == OK
 
 
@@ -79,7 +79,7 @@ def test_combine_backward(lib):
     for kw in ({"dy": None}, {"map": None}, {"d": None}, {"dd": None, "dw": None}):
         assert f(**kw) == ERR_NULL, kw
     for n in ("dy", "d", "map", "w", "dd", "dw"):
-        assert f(**{n: P + 4}) == ERR_ALIGN, n
+        assert f(**{n: P + (2 if n in ("map", "w", "dw") else 8)}) == ERR_ALIGN, n
     assert f(T=0, dy=None, d=None, map=None, dd=None, dw=None) == OK
 
 

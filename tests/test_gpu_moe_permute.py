@@ -205,6 +205,25 @@ def test_swiglu_backward_weights(T, E, k, I, kind):
         assert not host(dw).reshape(-1)[t2r < 0].any()
 
 
+def test_ids_maps_and_weights_that_start_anywhere():
+    T, E, k, H = 41, 9, 3, 64
+    x, _ = values((T, H), "bf16", 38, 1)
+    ids, w = routing("uniform", T, E, k, 38)
+    ref = pmg.moe_permute(x[1:].contiguous(), dev(ids[1:]), E)
+    i = lambda n: torch.empty(n + 3, dtype=torch.int32, device="cuda")[3:]
+    R = (T - 1) * k
+    got = pmg.moe_permute(x[1:], dev(ids)[1:], E, out={"expert_offsets": i(E + 1), "row_to_tk": i(R), "tk_to_row": i(R)})
+    for n in ref:
+        assert torch.equal(got[n], ref[n]), n
+    tw = dev(w)[1:]
+    assert torch.equal(pmg.moe_combine(ref["rows"], got["tk_to_row"], k, tw),
+                       pmg.moe_combine(ref["rows"], ref["tk_to_row"], k, tw.clone()))
+    dw = torch.empty(R + 1, dtype=torch.float32, device="cuda")[1:]
+    a = pmg.moe_combine_backward(x[1:], ref["rows"], got["tk_to_row"], k, tw, dw=dw)
+    b = pmg.moe_combine_backward(x[1:], ref["rows"], ref["tk_to_row"], k, tw.clone())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1].view(-1), b[1].view(-1))
+
+
 def test_empty_batches():
     e = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device="cuda")
     i = lambda *s: e(*s, dt=torch.int32)

@@ -155,6 +155,26 @@ def test_outputs_given_and_rows_do_not_depend_on_others():
     assert pmg.moe_router_topk_backward(w, ids, w, logits, dlogits=dl) is dl and not dl.isnan().any()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,k", [(5, 2), (37, 6), (250, 8), (301, 3)])
+def test_logits_that_start_anywhere(E, k, dtype):
+    """Tokens of a larger batch: views that start at any element."""
+    logits, v = logits_of(20, E, dtype, 28)
+    g = W.rng(29, E).standard_normal((20, k)).astype(np.float32)
+    flat = torch.empty(20 * E + 7, dtype=logits.dtype, device="cuda")
+    whole, _ = pmg.moe_router_topk(logits, k)
+    for at in (1, 3):
+        part = flat[at:at + 19 * E].view(19, E)
+        part.copy_(logits[1:])
+        for renorm in (True, False):
+            ids, w = check_forward(part, v[1:], k, renorm)
+            assert torch.equal(ids, whole[1:])
+            check_backward(part, v[1:], ids, w, g[1:], renorm)
+        dl = torch.full((20 * E + 7,), -7.0, dtype=logits.dtype, device="cuda")
+        pmg.moe_router_topk_backward(dev(g)[1:], ids, w, part, dlogits=dl[at:at + 19 * E].view(19, E))
+        assert (dl[:at] == -7).all() and (dl[at + 19 * E:] == -7).all() and (dl[at:at + 19 * E] != -7).all()
+
+
 def test_empty_and_refused():
     ids, w = pmg.moe_router_topk(torch.empty(0, 8, device="cuda"), 2)
     assert ids.shape == (0, 2) and w.shape == (0, 2)
