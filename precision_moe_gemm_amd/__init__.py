@@ -870,8 +870,9 @@ def moe_combine(d, tk_to_row, k: int, topk_w=None, y=None, out_dtype=None):
     (default) or float32 (out_dtype=torch.float32, or an f32 `y`).  Without weights: moe_permute's gradient."""
     dev = _head(d, "d", _BF16_F32, 2)
     T = _entries(tk_to_row, k, dev)
-    H = d.shape[1]
-    _arg(d, "d", _BF16_F32, dev, numel=T * k * H)
+    rows, H = d.shape
+    if rows < T * k:
+        raise ValueError(f"d holds {rows} rows, needs {T * k}")
     if topk_w is not None:
         _arg(topk_w, "topk_w", _F32, dev, numel=T * k)
     if out_dtype is None and y is None:

@@ -14,9 +14,8 @@
 // faster: with that read 117 us for 125 at 100 MB, 190 for 197 at 180 MB, 277 for 269 at 256 MB, 474 for 424
 // at 400 MB.
 //
-// Squares of bf16 and float32 values are exact in
-// float64, and their float64 sums, in an order that depends on the sizes and the alignment alone, are off
-// by far less than a float32 step, so the norm is rounded once.
+// Squares of bf16 and float32 values are exact in float64, and their float64 sums, in an order that depends on
+// the sizes and the alignment alone, are off by far less than a float32 step, so the norm is rounded once.
 #include <algorithm>
 #include <new>
 

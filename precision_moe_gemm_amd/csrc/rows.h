@@ -88,11 +88,6 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
 }
 
 // the wavefront's sum in every lane, added in a fixed order
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
-  return v;
-}
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);

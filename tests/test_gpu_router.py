@@ -84,7 +84,7 @@ def check_backward(logits, v, ids, w, g, renorm):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 2, 2), (5, 8, 8), (7, 16, 1), (9, 63, 4), (4, 64, 32), (61, 65, 6),
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 2, 2), (5, 8, 8), (7, 16, 1), (5, 16, 16), (3, 17, 17), (4, 32, 32), (9, 63, 4), (4, 64, 32), (61, 65, 6),
                                    (130, 128, 8), (33, 129, 32), (17, 250, 3), (9, 256, 8), (11, 257, 7), (5, 512, 32),
                                    (6, 513, 2), (3, 1000, 9), (4, 1024, 32)])
 def test_forward_and_backward(T, E, k, dtype):

@@ -176,6 +176,39 @@ def test_graph_replays_match_eager():
                 assert torch.equal(v.view(u8), ref[n].view(u8)), f"replay {rep}: {n}"
 
 
+def test_captured_calls_that_allocate():
+    """Outputs and workspaces left to the calls, inside a captured graph, for a short and a long routing list."""
+    for T in (50, 3000):
+        lg = [dev(W.router_logits(T, 16, 56 + j)) for j in range(2)]
+        x, dy = (bf16_dev(W.gaussian_bf16((T, 64), 1.0, 56, j)) for j in range(2))
+        logits = lg[0].clone()
+
+        def run():
+            ids, w = pmg.moe_router_topk(logits, 4)
+            p = pmg.moe_permute(x, ids, 16)
+            y = pmg.moe_combine(p["rows"], p["tk_to_row"], 4, w, out_dtype=torch.float32)
+            dd, dw = pmg.moe_combine_backward(dy, p["rows"], p["tk_to_row"], 4, w)
+            dl = pmg.moe_router_topk_backward(dw, ids, w, logits)
+            norm, out = pmg.grad_clip([dl, dd], 0.1)
+            return [ids, w, *p.values(), y, dd, dw, dl, norm, *out, pmg.grad_norm([dl])]
+
+        want = []
+        for v in lg:
+            logits.copy_(v)
+            want.append([t.clone() for t in run()])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = run()
+        for rep in range(4):
+            logits.copy_(lg[rep % 2])
+            junk = [torch.full_like(t, 3) for t in got]     # the program's own allocations in between
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want[rep % 2])), f"T={T} replay {rep}"
+            del junk
+
+
 def test_two_streams_at_once():
     a, b = Layer(300, 128, 16, 4, 64, 54), Layer(2000, 128, 64, 8, 64, 55, True)
     want = []
