@@ -18,6 +18,7 @@ import ctypes
 import math
 import os
 from array import array
+from operator import attrgetter, is_
 
 import torch
 
@@ -936,6 +937,7 @@ def grad_workspace_size(n: int) -> int:
     return int(load_library().moe_grad_workspace_size(n))
 
 
+_DTYPE = attrgetter("dtype")
 _GRAD_TYPES = {torch.float32: 1, **dict.fromkeys(_BF16, 0)}
 
 
@@ -944,9 +946,9 @@ def _grads(grads, what, dev):
     # models hold hundreds of tensors, so the checks run over the whole list; the loop names the one that fails
     if grads and all(isinstance(t, torch.Tensor) for t in grads):
         where = set(map(torch.Tensor.get_device, grads))
-        types = [_GRAD_TYPES.get(t.dtype, -1) for t in grads]
+        types = list(map(_GRAD_TYPES.get, map(_DTYPE, grads)))
         at = where.pop()
-        if not where and at >= 0 and dev in (None, at) and -1 not in types and all(map(torch.Tensor.is_contiguous, grads)):
+        if not where and at >= 0 and dev in (None, at) and None not in types and all(map(torch.Tensor.is_contiguous, grads)):
             return array("Q", map(torch.Tensor.data_ptr, grads)), array("i", types), array("q", map(torch.Tensor.numel, grads)), at
     for j, t in enumerate(grads):
         if dev is None:
@@ -956,25 +958,27 @@ def _grads(grads, what, dev):
 
 
 def _grad_buffers(n, norm, workspace, dev):
+    """The device, norm and workspace of a call on n tensors of device `dev` (None: no tensors)."""
+    if dev is None:
+        dev = torch.cuda.current_device() if norm is None else _head(norm, "norm", _F32, None)
     where = torch.device("cuda", dev)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=where)
     else:
         _arg(norm, "norm", _F32, dev, numel=1)
     if workspace is None:
-        workspace = torch.empty(max(grad_workspace_size(n), 256), dtype=torch.uint8, device=where)
+        workspace = torch.empty(grad_workspace_size(n) or 256, dtype=torch.uint8, device=where)
     else:
         _arg(workspace, "workspace", _U8, dev)
-    return norm, workspace
+    return dev, norm, workspace
 
 
 def grad_norm(grads, norm=None, workspace=None):
     """sqrt of the sum of squares over all elements of the tensors (bf16 or f32, any shapes and alignment):
     a float32 device tensor [1]."""
     grads = list(grads)
-    ptrs, types, sizes, dev = _grads(grads, "grads", None if norm is None else norm.get_device())
-    dev = torch.cuda.current_device() if dev is None else dev
-    norm, workspace = _grad_buffers(len(grads), norm, workspace, dev)
+    ptrs, types, sizes, dev = _grads(grads, "grads", None)
+    dev, norm, workspace = _grad_buffers(len(grads), norm, workspace, dev)
     _call("moe_grad_norm", dev, *(a.buffer_info()[0] for a in (ptrs, types, sizes)), len(grads), norm.data_ptr(),
           workspace.data_ptr(), workspace.numel())
     return norm
@@ -984,15 +988,16 @@ def grad_clip(grads, max_norm: float, out=None, norm=None, workspace=None):
     """Scale the tensors by min(1, max_norm / (norm + 1e-6)), norm as grad_norm's: (norm f32 [1], out).
     `out`: tensors of the same sizes and types; `out=grads` clips in place; None: new ones."""
     grads = list(grads)
-    ptrs, types, sizes, dev = _grads(grads, "grads", None if norm is None else norm.get_device())
-    dev = torch.cuda.current_device() if dev is None else dev
+    ptrs, types, sizes, dev = _grads(grads, "grads", None)
     out = [torch.empty_like(t) for t in grads] if out is None else list(out)
     if len(out) != len(grads):
         raise ValueError(f"{len(out)} outputs for {len(grads)} tensors")
-    outs, otypes, osizes, _ = _grads(out, "out", dev)
-    if otypes != types or osizes != sizes:
-        raise ValueError("out must have the sizes and types of grads")
-    norm, workspace = _grad_buffers(len(grads), norm, workspace, dev)
+    outs = ptrs
+    if not all(map(is_, out, grads)):
+        outs, otypes, osizes, _ = _grads(out, "out", dev)
+        if otypes != types or osizes != sizes:
+            raise ValueError("out must have the sizes and types of grads")
+    dev, norm, workspace = _grad_buffers(len(grads), norm, workspace, dev)
     _call("moe_grad_clip", dev, *(a.buffer_info()[0] for a in (ptrs, outs, types, sizes)), len(grads), max_norm,
           norm.data_ptr(), workspace.data_ptr(), workspace.numel())
     return norm, out

@@ -185,7 +185,7 @@ __global__ __launch_bounds__(kRouteThreads) void permute_kernel(
 // Short routing lists in one launch: every workgroup reads the whole list, counts each expert's entries and
 // those before its own (LDS; sums of whole numbers, whose order changes nothing), scans the counts, and ranks the entries of its own `per` tokens; its
 // wavefronts then take one (token, slot) row each.
-constexpr int kShort = 6144;            // entries; 128 experts, in one launch and in two: 3072 entries 7.5 us
+constexpr int kShort = 6144;            // entries; 128 experts, in one launch and in two: 3200 entries 7.2 us
                                         // for 9.8, 6144 10.0 for 10.8, 8192 12.2 for 12.2, 16384 21.9 for 19.2
 constexpr int kShortTokens = 8;         // most tokens a workgroup
 __global__ __launch_bounds__(kRouteThreads) void permute_short_kernel(

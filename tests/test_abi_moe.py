@@ -147,12 +147,12 @@ def test_binding_refusals():
     f, i = torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32)
     for call in (lambda: pmg.moe_router_topk(f, 2), lambda: pmg.moe_router_topk_backward(f, i, f, f),
                  lambda: pmg.moe_permute(f, i, 4), lambda: pmg.moe_combine(f, i, 2),
-                 lambda: pmg.moe_combine_backward(f, f, i, 2), lambda: pmg.grad_norm([f]), lambda: pmg.grad_clip([f], 1.0),
+                 lambda: pmg.moe_combine_backward(f, f, i, 2), lambda: pmg.grad_norm([f]), lambda: pmg.grad_clip([f], 1.0), lambda: pmg.grad_norm([], norm=f),
                  lambda: pmg.swiglu_backward_weights(f, f, i, f, i, i)):
         with pytest.raises(ValueError, match="device tensor"):
             call()
     for call in (lambda: pmg.moe_router_topk(f.half(), 2), lambda: pmg.moe_router_topk(None, 2),
                  lambda: pmg.moe_permute(f, f, 4), lambda: pmg.grad_norm([1.0]), lambda: pmg.grad_norm([f.double()]),
-                 lambda: pmg.moe_combine_backward(None, f, i, 2)):
+                 lambda: pmg.moe_combine_backward(None, f, i, 2), lambda: pmg.grad_norm([], norm=1.0)):
         with pytest.raises(TypeError):
             call()
