@@ -52,6 +52,9 @@ def check(grads, max_norm, out=None):
 SPECS = {
     "one": [(1, "f32")],
     "one_bf16": [(1, "bf16")],
+    "two": [(1000, "bf16"), (0, "f32"), (333, "f32")],
+    "two_pieces": [(30_000, "f32")],
+    "two_full_pieces": [(65_550, "bf16")],
     "small": [(3, "bf16"), (0, "f32"), (5, "f32"), (8, "bf16"), (4, "f32"), (7, "f32"), (9, "bf16"), (64, "f32")],
     "odd": [(1021, "f32"), (4099, "bf16"), (16385, "f32"), (32769, "bf16"), (65537, "f32")],
     "many": [(1 + 37 * j % 900, "f32" if j % 3 else "bf16") for j in range(230)],
