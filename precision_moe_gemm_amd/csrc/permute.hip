@@ -241,30 +241,19 @@ __global__ __launch_bounds__(kRouteThreads) void permute_short_kernel(
   }
 }
 
-// Short rows leave most of a wavefront without columns, so a group of lanes takes an item (a token, a routed
-// entry): the least power of two that holds the row 8 elements a lane, at most a wavefront (16384 tokens x 8
-// rows of 64 bf16: the combine 5.0 us and its gradient 7.9, with a wavefront an item 14.3 and 44.8).
-inline int log_lanes_for(int64_t words) {
-  int lg = 0;
-  while (lg < 6 && (1 << lg) < words) ++lg;
-  return lg;
-}
-
-// One group of 2^lg lanes per 8 * 2^lg columns of a token's sum, taken in FP32 and in slot order with products
-// and sums rounded apart; the loads of 8 slots are issued before the first is added.  They are non-temporal:
-// each row is read once (4096 tokens x 8 rows of 2048 bf16: 27 us for 29; 151 MB, so 5.6 TB/s).  Every lane
-// reads the token's rows and weights itself (handed round a wavefront with shuffles they take 26.2 us for 26.5
-// there, 36.9 for 34.4 at 16384 tokens with 2 rows).
+// One lane per 8 columns of a token's sum, taken in FP32 and in slot order with products and sums rounded apart;
+// the loads of 8 slots are issued before the first is added.  They are non-temporal: each row is read once (4096
+// tokens x 8 rows of 2048 bf16: 27 us for 29; 151 MB, so 5.6 TB/s).  Every lane reads the token's rows and
+// weights itself (handed round a wavefront with shuffles they take 26.2 us for 26.5 there, 36.9 for 34.4 at
+// 16384 tokens with 2 rows), so that a wavefront may go over from one token to the next and no lane is without
+// columns, whatever the row's length (16384 tokens x 8 rows of 520 bf16: 30 us, 34 with whole wavefronts a token).
 template <bool DF32, bool YF32>
 __global__ __launch_bounds__(kThreads) void combine_kernel(
-    const void* __restrict__ d, int T, int k, int H, int lg, const int32_t* __restrict__ tk_to_row,
+    const void* __restrict__ d, int T, int k, int H, const int32_t* __restrict__ tk_to_row,
     const float* __restrict__ topk_w, void* __restrict__ y) {
-  const uint32_t pieces = (uint32_t)(H + (8 << lg) - 1) >> (lg + 3);
-  const uint32_t item = (blockIdx.x * kThreads + threadIdx.x) >> lg, t = item / pieces;
+  const uint32_t words = (uint32_t)H / 8, item = blockIdx.x * kThreads + threadIdx.x, t = item / words;
   if (t >= (uint32_t)T) return;
-  const int lane = threadIdx.x & ((1 << lg) - 1);
-  const int c = (int)(((item - t * pieces) << lg) + lane) * 8, R = T * k;
-  if (c >= H) return;
+  const int c = (int)(item - t * words) * 8, R = T * k;
   const int32_t* map = tk_to_row + (int64_t)t * k;
   const float* wt = topk_w ? topk_w + (int64_t)t * k : nullptr;
   float acc[8] = {};
@@ -296,6 +285,18 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(
     }
   }
   store8<YF32>(y, (int64_t)t * H + c, acc);
+}
+
+// Lanes that take an entry's row, a power of two: as many as hold it 8 elements a lane, up to a wavefront; half a
+// wavefront for the rows just longer than that, of which a wavefront's second step would have few (16384 tokens
+// x 8 rows of 64 bf16 7.8 us, with a wavefront a row 44.8; of 520, 61.8 and 79.5; but of 264 float32, which a
+// wavefront holds, 72 us, 83 with 16 lanes).
+constexpr int kAhead = 4;
+inline int log_lanes_for(int64_t words) {
+  if (words > 64) return words <= 96 ? 5 : 6;
+  int lg = 0;
+  while ((1 << lg) < words) ++lg;
+  return lg;
 }
 
 // One group of 2^lg lanes per entry i = (t, s): dd[row] = w_i dy[t], dw_i = <dy[t], d[row]> in FP32, added within
@@ -419,14 +420,16 @@ NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t 
     return launch_status();
   }
   const int rounds = mp::rounds_of(T, k);
+  int group = 1;                                  // lanes that hold a short row, repeated over the wavefront
+  while (group < kWave && group < words) group *= 2;
   const unsigned grid = (unsigned)((T + kRouteTokens * rounds - 1) / (kRouteTokens * rounds));
   if ((int64_t)chunks * E <= kCountTable) {
     mp::permute_kernel<true><<<grid, kRouteThreads, 0, s>>>(src, T, words, topk_ids, k, E, table, rank, nullptr, chunks,
-        mp::kChunkLog, rounds, 1 << mp::log_lanes_for(words), dst, expert_offsets, row_to_tk, tk_to_row);
+        mp::kChunkLog, rounds, group, dst, expert_offsets, row_to_tk, tk_to_row);
   } else {
     mp::route_columns_kernel<<<(E + kWave - 1) / kWave, mp::kColumnWaves * 64, 0, s>>>(table, chunks, E, total);
     mp::permute_kernel<false><<<grid, kRouteThreads, 0, s>>>(src, T, words, topk_ids, k, E, table, rank, total, chunks,
-        mp::kChunkLog, rounds, 1 << mp::log_lanes_for(words), dst, expert_offsets, row_to_tk, tk_to_row);
+        mp::kChunkLog, rounds, group, dst, expert_offsets, row_to_tk, tk_to_row);
   }
   return launch_status();
 }
@@ -440,12 +443,11 @@ NVFP4MOE_API int moe_combine(const void* d, int32_t d_dtype, int64_t T, int32_t 
   if (!d || !tk_to_row || !y) return NVFP4_ERR_NULL;
   if (!aligned16(d) || !aligned16(y) || !aligned_to(tk_to_row, 4) || !aligned_to(topk_w, 4)) return NVFP4_ERR_ALIGN;
   if (d == y) return NVFP4_ERR_ARG;
-  const int lg = mp::log_lanes_for(H / 8), per = mp::kThreads >> lg;
-  const int64_t items = T * ((H + (8 << lg) - 1) >> (lg + 3));
-  const unsigned grid = (unsigned)((items + per - 1) / per);
+  // at most 2^32 - 1024 lanes, by the limit above
+  const unsigned grid = (unsigned)((T * (H / 8) + mp::kThreads - 1) / mp::kThreads);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool df = d_dtype == NVFP4_IN_F32, yf = y_dtype == NVFP4_IN_F32;
-#define MP_COMBINE(D, Y) mp::combine_kernel<D, Y><<<grid, mp::kThreads, 0, s>>>(d, (int)T, k, (int)H, lg, tk_to_row, topk_w, y)
+#define MP_COMBINE(D, Y) mp::combine_kernel<D, Y><<<grid, mp::kThreads, 0, s>>>(d, (int)T, k, (int)H, tk_to_row, topk_w, y)
   if (df) yf ? MP_COMBINE(true, true) : MP_COMBINE(true, false);
   else yf ? MP_COMBINE(false, true) : MP_COMBINE(false, false);
 #undef MP_COMBINE
@@ -475,8 +477,8 @@ NVFP4MOE_API int moe_combine_backward(const void* dy, int32_t dy_dtype, const vo
                                                                         topk_w, dd, dtopk_w)
 #define MP_BACKWARD_BY(Y, D)                                                                            \
   do {                                                                                                  \
-    if (H <= 512) streamed ? MP_BACKWARD(Y, D, true, 1) : MP_BACKWARD(Y, D, false, 1);                  \
-    else streamed ? MP_BACKWARD(Y, D, true, 4) : MP_BACKWARD(Y, D, false, 4);                           \
+    if (H <= 8 << lg) streamed ? MP_BACKWARD(Y, D, true, 1) : MP_BACKWARD(Y, D, false, 1);              \
+    else streamed ? MP_BACKWARD(Y, D, true, mp::kAhead) : MP_BACKWARD(Y, D, false, mp::kAhead);         \
   } while (0)
   if (yf) { if (df) MP_BACKWARD_BY(true, true); else MP_BACKWARD_BY(true, false); }
   else { if (df) MP_BACKWARD_BY(false, true); else MP_BACKWARD_BY(false, false); }
