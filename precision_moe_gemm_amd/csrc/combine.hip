@@ -211,10 +211,12 @@ void launch_swiglu_backward(const float* gu, const float* dh, int64_t R_cap, int
                             const float* topk_w, const int32_t* row_to_tk, uint16_t* dgu, const int32_t* tk_to_row,
                             float* dw, hipStream_t s) {
   // the least power of two of lanes that holds the row 4 elements a lane, at most a wavefront (131072 rows of
-  // 16: 11 us, of 64: 29, with a wavefront a row 92 and 93; narrower groups that go over a longer row more
+  // 16: 11 us, of 64: 29, with a wavefront a row 92 and 93), half a wavefront for rows just longer than its 256
+  // elements (65536 rows of 264 67 us for 88, of 384 73 for 93; narrower groups that go over longer rows more
   // often take longer, 97 us for 65 at 32768 rows of 520)
   int lg = 0;
   while (lg < 6 && (4 << lg) < I) ++lg;
+  if (I > 256 && I <= 384) lg = 5;
   const int rows = 256 >> lg;
   const unsigned grid = (unsigned)((R_cap + rows - 1) / rows);
   if (R_cap >= kLastLevelCache / (16 * I))

@@ -3,8 +3,8 @@
 The permutation, the combine (FP32 in slot order, bf16 rounded once) and dd (one FP32 product, rounded once
 to bf16) are bit-exact.  A dot product dw over H elements is taken by 32 or 64 lanes (fewer only where each has
 8 elements): at most 8 ceil(H / 256) sums in a lane and six levels over the lanes, each rounded (2^-24):
-(8 ceil(H / 256) + 6) 2^-24 sum |dy d|.  The SwiGLU's dw is
-summed in float64 with terms within 2^-49 of theirs and rounded once: 2^-24 |dw| + 2^-45 sum |terms|.
+(8 ceil(H / 256) + 6) 2^-24 sum |dy d|.  The SwiGLU's dw is summed in float64 with terms within 2^-49 of theirs
+and rounded once: 2^-24 |dw| + 2^-45 sum |terms|.
 """
 import numpy as np
 import pytest
@@ -184,7 +184,7 @@ def test_bad_map_entries_are_skipped():
 
 
 @pytest.mark.parametrize("T,E,k,I,kind", [(1, 128, 8, 768, "softmax"), (61, 128, 8, 768, "uniform"), (257, 24, 4, 264, "zipf"),
-                                          (40, 64, 32, 8, "uniform"), (9, 4, 2, 2056, "uniform"), (5, 1, 1, 256, "uniform")])
+                                          (40, 64, 32, 8, "uniform"), (33, 16, 4, 384, "uniform"), (17, 8, 2, 128, "zipf"), (9, 4, 2, 2056, "uniform"), (5, 1, 1, 256, "uniform")])
 def test_swiglu_backward_weights(T, E, k, I, kind):
     print(f"[swiglu backward] T={T} E={E} k={k} I={I} {kind}", flush=True)
     R = T * k
