@@ -642,9 +642,11 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  * moe_grad_clip - the norm, and out_j = grads_j * c with c = min(1, max_norm / (norm + 1e-6)),
  * factor and products in FP64, rounded to float (and from there to bf16).  out: HOST array of n device
  * pointers; out_j is grads_j itself (in place) or memory that overlaps no other tensor of
- * the call (NVFP4_ERR_ARG).  A norm that is inf gives c = 0, a NaN one c = NaN.
- * Requires max_norm >= 0 (inf: the norm alone, and a copy where not in place),
- * n <= MOE_MAX_TENSORS and at most MOE_MAX_GRAD_BYTES bytes of tensors.
+ * the call (NVFP4_ERR_ARG).  c is formed from the norm in FP64, before it is rounded to float: 0 where
+ * that is inf (so that infinities become NaN and all else 0), NaN where it is NaN, above 0 where the
+ * float alone overflows.  max_norm = inf takes the norm alone: c = 1 whatever the norm, tensors in
+ * place keep their bits, others are copied (a NaN as a NaN).
+ * Requires max_norm >= 0, n <= MOE_MAX_TENSORS and at most MOE_MAX_GRAD_BYTES bytes of tensors.
  */
 #define MOE_MAX_ROWS ((1 << 26) - 16)   /* T * k: what one launch holds */
 #define MOE_MAX_H (1 << 20)

@@ -6,7 +6,8 @@ Maps as in ``oracle.permute``; everything in float64.
   * combine: y[t] = sum_s w_i D[row(i)], i = t k + s.  dD[row(i)] = w_i dy[t]; dw_i = <dy[t], D[row(i)]>, 0
     for an entry without a row; rows that no entry names keep what they hold.
   * SwiGLU: h = w silu(g) u per row; dw of the row's entry = sum_j dh_j silu(g_j) u_j.
-  * norm: sqrt of the sum of squares over all tensors; clipping multiplies by min(1, max_norm / (norm + 1e-6)).
+  * norm: sqrt of the sum of squares over all tensors; clipping multiplies by min(1, max_norm / (norm + 1e-6)),
+    with max_norm = inf (the norm alone) by 1 whatever the norm.
 """
 from __future__ import annotations
 
@@ -56,6 +57,8 @@ def norm(tensors) -> float:
 
 def clip(tensors, max_norm: float):
     n = norm(tensors)
+    if max_norm == np.inf:
+        return n, [np.asarray(t, np.float64) for t in tensors]
     with np.errstate(invalid="ignore"):
         c = np.float64(max_norm) / (np.float64(n) + 1e-6)
     c = 1.0 if c >= 1.0 else c

@@ -986,7 +986,8 @@ def grad_norm(grads, norm=None, workspace=None):
 
 def grad_clip(grads, max_norm: float, out=None, norm=None, workspace=None):
     """Scale the tensors by min(1, max_norm / (norm + 1e-6)), norm as grad_norm's: (norm f32 [1], out).
-    `out`: tensors of the same sizes and types; `out=grads` clips in place; None: new ones."""
+    `out`: tensors of the same sizes and types; `out=grads` clips in place; None: new ones.
+    max_norm=inf: the norm alone (a factor of 1 whatever the norm)."""
     grads = list(grads)
     ptrs, types, sizes, dev = _grads(grads, "grads", None)
     out = [torch.empty_like(t) for t in grads] if out is None else list(out)

@@ -196,8 +196,10 @@ __device__ __forceinline__ void scale_piece(const void* in, void* out, int64_t n
   }
 }
 
-// min(1, max_norm / (norm + 1e-6)), NaN for a NaN norm
+// min(1, max_norm / (norm + 1e-6)), NaN for a NaN norm; max_norm = inf asks for the norm alone: 1, also where the
+// norm is inf (inf / inf would be NaN) or NaN
 __device__ __forceinline__ double factor_of(double norm, double max_norm) {
+  if (max_norm == INFINITY) return 1.0;
   const double ratio = max_norm / (norm + 1e-6);
   return ratio >= 1.0 ? 1.0 : ratio;
 }
