@@ -4,8 +4,10 @@
 //
 // The tensors' addresses go to the kernels by value, kTensors a launch, so that no table has to be copied
 // to the device first.  A launch's work is cut into pieces of kPiece bytes (131072: 1.06 ms).  For the norm,
-// workgroup b of at most kPartials (256: 1.18 ms, 2048: 1.04 ms) takes pieces b, b + grid, ... and leaves one
-// partial sum of squares.  The clipping workgroups take one piece each (2048 workgroups that take many: 1.11
+// workgroup b of at most kPartials a launch (256: 1.18 ms, 2048: 1.04 ms) takes pieces b, b + grid, ... and adds
+// its sum of squares to the one that workgroup b of the launches before it left: launches run one after another,
+// so each has to fill the device by itself (2.15 GB as 6 tensors 333 us, as 400, 1000 and 4000 344, 377 and 550;
+// with 1024 workgroups shared out over the launches 613, 1256 and 5160).  The clipping workgroups take one piece each (2048 workgroups that take many: 1.11
 // ms for 1.09) and add the partial sums up themselves, all in the same order.  Loads run kAhead words ahead
 // (1 instead of 4: 1.17 ms for 1.14).
 //
@@ -29,7 +31,7 @@ constexpr int kTensors = 96;          // tensors a launch (the kernel arguments 
 constexpr int kThreads = 256;
 constexpr int kPiece = 65536;         // bytes of a piece, 16-byte words of one tensor
 constexpr int kPieceWords = kPiece / 16;
-constexpr int kPartials = 1024;       // norm workgroups over all launches (more where launches are more)
+constexpr int kPartials = 1024;       // most norm workgroups of a launch, and partial sums of all of them
 constexpr int kAhead = 4;
 
 struct Table {
@@ -127,8 +129,9 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return s;
 }
 
+// used: the partial sums that launches before this one have written; the others are written here for the first time
 template <bool STREAM>
-__global__ __launch_bounds__(kThreads) void squares_kernel(const Table t, double* __restrict__ partial) {
+__global__ __launch_bounds__(kThreads) void squares_kernel(const Table t, int used, double* __restrict__ partial) {
   __shared__ double lds[kThreads / kWave];
   double acc = 0.0;
   for (int p = blockIdx.x; p < t.first[t.n]; p += gridDim.x) {
@@ -137,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void squares_kernel(const Table t, double
                       : piece_squares<false, STREAM, kThreads>(t.in[q.j], t.numel[q.j], q);
   }
   acc = block_sum(acc, lds);
-  if (threadIdx.x == 0) partial[blockIdx.x] = acc;
+  if (threadIdx.x == 0) partial[blockIdx.x] = (int)blockIdx.x < used ? partial[blockIdx.x] + acc : acc;
 }
 
 // The norm from n partial sums, in every thread, in an order that is the same in every workgroup.
@@ -248,9 +251,6 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(const Table t, dou
 }
 
 // ------------------------------------------------------------------ host
-inline int launches_of(int64_t n) { return (int)((n + kTensors - 1) / kTensors); }
-inline int blocks_each(int64_t n) { return std::max(1, kPartials / std::max(1, launches_of(n))); }
-
 int check(const void* const* in, const int32_t* dtype, const int64_t* numel, int32_t n) {
   if (n < 0 || n > MOE_MAX_TENSORS) return NVFP4_ERR_SHAPE;
   if (n && (!in || !dtype || !numel)) return NVFP4_ERR_NULL;
@@ -316,7 +316,6 @@ int fill(Table& t, const void* const* in, void* const* out, const int32_t* dtype
 int run(const void* const* in, void* const* out, const int32_t* dtype, const int64_t* numel, int32_t n, double max_norm,
         float* norm, double* partial, hipStream_t s) {
   Table t;
-  const int most = blocks_each(n);
   int used = 0;
   int64_t bytes = 0;
   for (int i = 0; i < n; ++i) bytes += numel[i] * (dtype[i] == NVFP4_IN_F32 ? 4 : 2);
@@ -329,10 +328,10 @@ int run(const void* const* in, void* const* out, const int32_t* dtype, const int
   for (int i = 0; i < n;) {
     i = fill(t, in, out, dtype, numel, i, n);
     if (!t.n) break;
-    const int grid = std::min(most, t.first[t.n]);
-    if (stream) squares_kernel<true><<<grid, kThreads, 0, s>>>(t, partial + used);
-    else squares_kernel<false><<<grid, kThreads, 0, s>>>(t, partial + used);
-    used += grid;
+    const int grid = std::min(kPartials, t.first[t.n]);
+    if (stream) squares_kernel<true><<<grid, kThreads, 0, s>>>(t, used, partial);
+    else squares_kernel<false><<<grid, kThreads, 0, s>>>(t, used, partial);
+    used = std::max(used, grid);
   }
   if (!out || !used) {
     norm_kernel<<<1, kThreads, 0, s>>>(partial, used, norm);
@@ -358,7 +357,7 @@ extern "C" {
 
 NVFP4MOE_API size_t moe_grad_workspace_size(int32_t n) {
   if (n < 0 || n > MOE_MAX_TENSORS) return 0;
-  return (size_t)std::max(gc::kPartials, gc::launches_of(n)) * sizeof(double);
+  return gc::kPartials * sizeof(double);
 }
 
 NVFP4MOE_API int moe_grad_norm(const void* const* grads, const int32_t* dtypes, const int64_t* numel, int32_t n,
