@@ -604,9 +604,10 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  * moe_permute - nvfp4_quantize_permute's routing for rows that are not quantised here:
  * expert_offsets, row_to_tk and tk_to_row exactly as it writes them, and
  *     rows[tk_to_row[t*k+s]] = x[t]   (copied bits)
- *   x [T][H] of x_dtype; rows out [T*k][H]; both NULL: the maps alone (H and x_dtype unused)
- *   workspace: moe_permute_workspace_size(T, k, E) bytes (0 for short routing lists: NULL),
- *   used as nvfp4_quantize_permute uses its own; dev_err as there
+ *   x [T][H] of x_dtype; rows out [T*k][H]; both NULL: the maps alone (H unused)
+ *   workspace: moe_permute_workspace_size(T, k, E) bytes (0 for short routing lists: NULL), used as
+ *   nvfp4_quantize_permute uses its own; T = 0 uses none, whatever the function gives, so that what
+ *   serves a batch serves every smaller one.  dev_err as there
  * rows and row_to_tk at or beyond expert_offsets[E] are left as they were.  Requires
  * H % 8 == 0, 8 <= H <= MOE_MAX_H, 1 <= k <= min(E, NVFP4MOE_MAX_TOPK), 1 <= E <=
  * NVFP4MOE_MAX_EXPERTS, T * k <= MOE_MAX_ROWS.

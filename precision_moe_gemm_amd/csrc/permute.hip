@@ -391,7 +391,7 @@ NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t 
   if (!mp::type_ok(x_dtype)) return NVFP4_ERR_ARG;
   if (const int bad = mp::check(T, k, x || rows ? H : 8)) return bad;
   if (E < 1 || E > NVFP4MOE_MAX_EXPERTS || k > E) return NVFP4_ERR_SHAPE;
-  const size_t need = moe_permute_workspace_size(T, k, E);
+  const size_t need = T > 0 ? moe_permute_workspace_size(T, k, E) : 0;
   if (!expert_offsets || (need && !workspace)) return NVFP4_ERR_NULL;
   if (T > 0 && (!topk_ids || !row_to_tk || !tk_to_row || !x != !rows)) return NVFP4_ERR_NULL;
   if (!aligned16(x) || !aligned16(rows) || !aligned16(workspace) || !aligned_to(topk_ids, 4) ||
@@ -404,9 +404,9 @@ NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t 
   const int words = (int)(H * (x_dtype == NVFP4_IN_F32 ? 4 : 2) / 16);
   const uint4* src = static_cast<const uint4*>(x);
   uint4* dst = static_cast<uint4*>(rows);
-  if (T > 0 && n <= mp::kShort) {
-    const int per = (int)std::min<int64_t>(mp::kShortTokens, (T + 255) / 256);
-    mp::permute_short_kernel<<<(unsigned)((T + per - 1) / per), kRouteThreads, 0, s>>>(
+  if (n <= mp::kShort) {                          // T = 0: one workgroup, which writes the offsets
+    const int per = (int)std::clamp<int64_t>((T + 255) / 256, 1, mp::kShortTokens);
+    mp::permute_short_kernel<<<(unsigned)std::max<int64_t>(1, (T + per - 1) / per), kRouteThreads, 0, s>>>(
         src, (int)T, words, topk_ids, k, E, per, dst, expert_offsets, row_to_tk, tk_to_row, dev_err);
     return launch_status();
   }
@@ -415,10 +415,6 @@ NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t 
   int32_t* total = table + (int64_t)chunks * E;             // [E]
   int32_t* rank = total + E;                                // [n]
   route_rank_kernel<<<chunks, kPlanThreads, 0, s>>>(topk_ids, (int)n, E, mp::kChunkLog, table, rank, dev_err);
-  if (T == 0) {
-    route_scan_kernel<<<1, kPlanThreads, 0, s>>>(table, chunks, E, expert_offsets);
-    return launch_status();
-  }
   const int rounds = mp::rounds_of(T, k);
   int group = 1;                                  // lanes that hold a short row, repeated over the wavefront
   while (group < kWave && group < words) group *= 2;
