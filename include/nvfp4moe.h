@@ -620,7 +620,7 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  *
  * moe_combine_backward - its gradient:
  *     dd[tk_to_row[i]] = w_i dy[t]               (i = t*k+s; w_i = 1 when topk_w is NULL)
- *     dtopk_w[i] = sum_h dy[t][h] d[tk_to_row[i]][h]   in FP32; 0 for an entry without a row
+ *     dtopk_w[i] = sum_h dy[t][h] d[tk_to_row[i]][h]   in FP64, rounded once; 0 for an entry without a row
  *   dy [T][H] of dy_dtype; d and dd [T*k][H] of d_dtype; dtopk_w float [T*k].  dd or
  *   dtopk_w may be NULL (not computed), d too without dtopk_w.  Rows that no entry names
  *   are left as they were.  tk_to_row names each row at most once.
