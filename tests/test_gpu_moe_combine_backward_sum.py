@@ -1,7 +1,7 @@
 """moe_combine_backward's router-weight gradient over long rows.
 
-Products and sums in FP64, rounded once: 2^-24 |dw| for the rounding and H 2^-53 sum |dy d| for the sums, whatever
-the row's length.  Rows whose products cancel show a sum that was rounded on the way.
+Products and sums in FP64, rounded once: 2^-24 |dw| for the rounding, and H 2^-53 sum |dy d| for the kernel's
+sums and as much for the reference's.  Rows whose products cancel show a sum that was rounded on the way.
 """
 import pytest
 import torch
