@@ -608,7 +608,8 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  *   workspace: moe_permute_workspace_size(T, k, E) bytes (0 for short routing lists: NULL), used as
  *   nvfp4_quantize_permute uses its own; T = 0 uses none, whatever the function gives, so that what
  *   serves a batch serves every smaller one.  dev_err as there
- * rows and row_to_tk at or beyond expert_offsets[E] are left as they were.  Requires
+ * rows and row_to_tk at or beyond expert_offsets[E] are left as they were.  The maps and offsets may
+ * not be topk_ids or each other (NVFP4_ERR_ARG).  Requires
  * H % 8 == 0, 8 <= H <= MOE_MAX_H, 1 <= k <= min(E, NVFP4MOE_MAX_TOPK), 1 <= E <=
  * NVFP4MOE_MAX_EXPERTS, T * k <= MOE_MAX_ROWS.
  * Its gradient is moe_combine without weights.

@@ -401,6 +401,10 @@ NVFP4MOE_API int moe_permute(const void* x, int32_t x_dtype, int64_t T, int64_t 
     return NVFP4_ERR_ALIGN;
   if (x && x == rows) return NVFP4_ERR_ARG;
   if (workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
+  // a short list's workgroups all read the ids while others write the maps
+  if (T > 0 && (row_to_tk == tk_to_row || expert_offsets == row_to_tk || expert_offsets == tk_to_row ||
+                topk_ids == row_to_tk || topk_ids == tk_to_row || topk_ids == expert_offsets))
+    return NVFP4_ERR_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t n = T * (int64_t)k;
   const int words = (int)(H * (x_dtype == NVFP4_IN_F32 ? 4 : 2) / 16);
