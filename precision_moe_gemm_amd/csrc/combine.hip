@@ -321,7 +321,8 @@ NVFP4MOE_API int swiglu_backward_weights(const float* gu, const float* dh, int64
   if (R_cap == 0) return NVFP4_OK;
   if (!gu || !dh || !expert_offsets || !topk_w || !row_to_tk || !tk_to_row || !dgu || !dtopk_w) return NVFP4_ERR_NULL;
   if (!aligned16(gu) || !aligned16(dh) || !aligned16(dgu) || !aligned_to(dtopk_w, 4)) return NVFP4_ERR_ALIGN;
-  if (dtopk_w == topk_w) return NVFP4_ERR_ARG;
+  const void* out = dgu;
+  if (dtopk_w == topk_w || out == gu || out == dh) return NVFP4_ERR_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
   launch_swiglu_backward<true>(gu, dh, R_cap, I, expert_offsets, E, topk_w, row_to_tk, dgu, tk_to_row, dtopk_w, s);
   return launch_status();

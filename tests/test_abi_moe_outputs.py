@@ -16,3 +16,11 @@ def test_permute(lib, T, same):
             continue
         assert lib.moe_permute(x, 0, T, 64, a["ids"], 8, 128, rows, a["off"], a["r2t"], a["t2r"], a["ws"], 1 << 30,
                                None, None) == ERR_ARG
+
+
+@pytest.mark.parametrize("same", [("gu", "dgu"), ("dh", "dgu"), ("w", "dw")])
+def test_swiglu_backward_weights(lib, same):
+    a = dict(zip(("gu", "dh", "off", "w", "r2t", "t2r", "dgu", "dw"), P))
+    a[same[1]] = a[same[0]]
+    assert lib.swiglu_backward_weights(a["gu"], a["dh"], 8, 64, a["off"], 4, a["w"], a["r2t"], a["t2r"], a["dgu"],
+                                       a["dw"], None) == ERR_ARG
