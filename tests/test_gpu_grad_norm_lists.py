@@ -79,3 +79,25 @@ def test_a_long_list_keeps_the_device_busy():
     many = _replay_us(list(flat.chunk(4096)))
     print(f"[norm] 1 GiB as 4 tensors {few:.0f} us, as 4096 {many:.0f} us", flush=True)
     assert many <= few + 43 * 15.0
+
+
+def test_captured_and_replayed():
+    """A list of several launches: each replay starts its partial sums anew."""
+    g = torch.Generator(device="cuda").manual_seed(74)
+    grads = [torch.randn(20_000 + 13 * j, generator=g, device="cuda") for j in range(300)]
+    out = [torch.empty_like(x) for x in grads]
+    norm = torch.empty(1, device="cuda")
+    ws = torch.empty(pmg.grad_workspace_size(len(grads)), dtype=torch.uint8, device="cuda")
+    pmg.grad_clip(grads, 1.0, out=out, norm=norm, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pmg.grad_clip(grads, 1.0, out=out, norm=norm, workspace=ws)
+    for scale in (1.0, 0.25, 3.0):
+        for x in grads:
+            x.mul_(scale)
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, clipped = pmg.grad_clip(grads, 1.0)
+        assert torch.equal(norm, want) and all(torch.equal(a, b) for a, b in zip(out, clipped))
