@@ -647,7 +647,8 @@ NVFP4MOE_API int bf16_grouped_gemm_wgrad(const uint16_t* g, int64_t g_rows, int3
  * the call (NVFP4_ERR_ARG).  c is formed from the norm in FP64, before it is rounded to float: 0 where
  * that is inf (so that infinities become NaN and all else 0), NaN where it is NaN, above 0 where the
  * float alone overflows.  max_norm = inf takes the norm alone: c = 1 whatever the norm, tensors in
- * place keep their bits, others are copied (a NaN as a NaN).
+ * place keep their bits, others are copied (a NaN as a NaN).  Where grads_j and out_j lie
+ * differently towards a 16-byte boundary, out_j is written element by element, a third slower.
  * Requires max_norm >= 0, n <= MOE_MAX_TENSORS and at most MOE_MAX_GRAD_BYTES bytes of tensors.
  */
 #define MOE_MAX_ROWS ((1 << 26) - 16)   /* T * k: what one launch holds */

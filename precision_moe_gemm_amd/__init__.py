@@ -830,7 +830,9 @@ def moe_permute_workspace_size(T: int, k: int, E: int) -> int:
 
 def moe_permute(x, topk_ids, E: int, workspace=None, dev_err=None, out=None):
     """Route + permute without quantising.  x bf16 or f32 [T, H], or None for the maps alone.  Returns dict
-    with rows [T*k, H] (x's type; not with x None), expert_offsets [E+1], row_to_tk [T*k], tk_to_row [T*k]."""
+    with rows [T*k, H] (x's type; not with x None), expert_offsets [E+1], row_to_tk [T*k], tk_to_row [T*k].
+    What lies in rows and row_to_tk at or behind expert_offsets[E] is not written: as it was in `out`, else
+    uninitialised."""
     dev = _head(topk_ids, "topk_ids", _I32T, 2)
     T, k = topk_ids.shape
     R, H = T * k, 0
@@ -987,7 +989,8 @@ def grad_norm(grads, norm=None, workspace=None):
 def grad_clip(grads, max_norm: float, out=None, norm=None, workspace=None):
     """Scale the tensors by min(1, max_norm / (norm + 1e-6)), norm as grad_norm's: (norm f32 [1], out).
     `out`: tensors of the same sizes and types; `out=grads` clips in place; None: new ones.
-    max_norm=inf: the norm alone (a factor of 1 whatever the norm)."""
+    max_norm=inf: the norm alone (a factor of 1 whatever the norm).  Outputs that lie towards a 16-byte
+    boundary as their tensors do are faster; new ones start at one, views into a flat buffer may not."""
     grads = list(grads)
     ptrs, types, sizes, dev = _grads(grads, "grads", None)
     out = [torch.empty_like(t) for t in grads] if out is None else list(out)

@@ -17,7 +17,9 @@ constexpr int kThreads = 256;
 // ones (in both cases after other work has left the caches full of lines to write back).  The grouped
 // product that reads them next gains less from their being cached than that: permutation and a BF16 gate_up
 // product together take 169 us for 176 at 600 tokens, 202 for 201 at 2048, 247 for 249 at 4096, 361 for 381
-// at 8192.
+// at 8192.  Short rows gain or lose little: 16384 tokens x 8 rows of 16 bytes 18.4 us for 18.0, of 64 17.6 for
+// 17.8, of 128 18.3 for 19.1, of 512 25.1 for 24.5, of 1024 37.8 for 41.8 (with a combine of the rows next 25.3
+// for 25.4, 22.6 for 23.8, 24.7 for 24.8, 40.4 for 37.6 and 64.7 for 59.1).
 __device__ __forceinline__ void store_row(uint4* dst, uint4 v) { store16<true>(dst, v); }
 
 // A wavefront's part of a token's row: its first kHeld 16-byte words a lane stay in registers (rows up to
@@ -187,8 +189,14 @@ __global__ __launch_bounds__(kRouteThreads) void permute_kernel(
 // Short routing lists in one launch: every workgroup reads the whole list, counts each expert's entries and
 // those before its own (LDS; sums of whole numbers, whose order changes nothing), scans the counts, and ranks
 // the entries of its own `per` tokens; its wavefronts then take one (token, slot) row each.
-constexpr int kShort = 6144;            // entries; 128 experts, in one launch and in two: 3200 entries 7.2 us
-                                        // for 9.8, 6144 10.0 for 10.8, 8192 12.2 for 12.2, 16384 21.9 for 19.2
+//
+// The border was measured at 128 experts and 8 slots, with rows of 4 KB (3200 entries in one launch and in two 7.2 us
+// for 9.8, 6144 10.0 for 10.8, 8192 12.2 for 12.2, 16384 21.9 for 19.2).  At 6144 entries, the maps alone, one
+// launch takes 7.1 to 7.3 us for 8.0 to 9.9 with 8 slots of 8 to 1024 experts, 7.9 for 9.8 with one slot of 128, 8.4
+// for 9.6 of 32; with one slot of 8 experts 10.9 for 9.3 and of 2 19.7 for 9.1 (two slots 13.2 for 8.4), because all
+// lanes add to the same few counters and more workgroups read the list: there two launches are faster from 5000 and
+// from 2500 entries on.
+constexpr int kShort = 6144;            // entries
 constexpr int kShortTokens = 8;         // most tokens a workgroup
 __global__ __launch_bounds__(kRouteThreads) void permute_short_kernel(
     const uint4* __restrict__ x, int T, int words, const int32_t* __restrict__ ids, int k, int E, int per,
@@ -247,6 +255,9 @@ __global__ __launch_bounds__(kRouteThreads) void permute_short_kernel(
 // weights itself (handed round a wavefront with shuffles they take 26.2 us for 26.5 there, 36.9 for 34.4 at
 // 16384 tokens with 2 rows), so that a wavefront may go over from one token to the next and no lane is without
 // columns, whatever the row's length (16384 tokens x 8 rows of 520 bf16: 30 us, 34 with whole wavefronts a token).
+// Of float32 rows to bf16, which unpermute_combine takes too and with the same bits: 61 tokens x 8 rows of 2048 4.9
+// us, its kernels 8.6; 1024 15.5 and 14.8; 4096 58.9 and 54.4, of 768 25.9 and 19.1, of 7168 204 and 208; 16384 of
+// 64 10.6 and 13.3, of 520 69 and 61.
 template <bool DF32, bool YF32>
 __global__ __launch_bounds__(kThreads) void combine_kernel(
     const void* __restrict__ d, int T, int k, int H, const int32_t* __restrict__ tk_to_row,

@@ -5,9 +5,12 @@
 // choice costs a group's reduction whatever the group's size, so that more tokens share it in the narrow
 // groups: 16381 x 250 bf16 logits, k = 6, take 6.6 us for 13.7 with a wavefront a token (8.2 MB read: 1.6 us
 // at a copy's rate), the gradient 8.3 for 11.8 (16.4 MB).  Of these a launch of one token takes 3.5 and 2.4,
-// the chain of its loads, rounds and stores; all the wavefronts of the larger case are resident at once and
-// run little more than one such chain.  (A shorter exp made no difference.)  Windows of 32 in narrow groups up
-// to 512 experts: 8192 x 512 bf16 5.7 us for 7.3, but float32 with its gradient 13.7 + 13.7 for 13.5 + 9.9.
+// the chain of its loads, rounds and stores.  Up to two wavefronts a SIMD run little more than one such chain;
+// beyond, the issue of their instructions shows (some 800 each, 4 cycles an instruction: 1.35 us a wavefront on a
+// SIMD): launches in a row in a graph, over all experts, take 4.9 us at one token, 5.1, 5.4, 5.6 and 5.9 at 1024,
+// 2048, 4096 and 8192, 7.8 at 16381, the gradient 5.2, 5.6, 5.7, 5.9, 7.1 and 10.0, with renorm 4.8, 4.7, 5.4, 5.4,
+// 5.6 and 6.2.  Windows of 32 in narrow groups up to 512 experts: 8192 x 512 bf16 5.7 us for 7.3, but float32 with
+// its gradient 13.7 + 13.7 for 13.5 + 9.9.
 #include "common.h"
 #include "fp8.h"
 #include "rows.h"
